@@ -217,7 +217,7 @@ def _prepare_attn(case, g):
         from routed_expert_ffn_amd import moe
         st["cache"] = moe.KVCache(k, v, ks, vs)
         # a serving loop keeps its workspace
-        st["ws"] = torch.empty(moe.paged_attention_workspace_size(rows, hq, hkv, D, S, W * P), dtype=torch.uint8,
+        st["ws"] = torch.empty(moe.paged_attention_workspace_size(rows, hq, hkv, D, S), dtype=torch.uint8,
                                device="cuda")
     return st
 
