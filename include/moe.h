@@ -74,7 +74,10 @@ typedef enum {
      * third bits, as words of 32 elements (element 16g + 4k + j of a word in
      * byte j, bit 4g + k). */
     MOE_INT2_B32 = 3,
-    MOE_INT3_B32 = 4
+    MOE_INT3_B32 = 4,
+    /* 8-bit floats of 4 exponent and 3 fraction bits (largest value 448, no
+     * infinities), for key-value caches (moe_kv_cache). */
+    MOE_FP8_E4M3 = 5
 } moe_dtype;
 
 typedef void* moe_stream; /* hipStream_t */
@@ -319,6 +322,138 @@ moe_status moe_strp_read(const void* buf, size_t bytes, int32_t* L, int32_t* E, 
                          uint16_t* pairs, int32_t pairs_capacity, int16_t* inverse, int64_t inverse_capacity);
 moe_status moe_profile_remap(const uint16_t* pairs, int32_t n, int32_t L, int32_t E_old, const int32_t* keep_map,
                              int32_t keep, uint16_t* out, int32_t* n_out);
+
+/* ---------------------------------------------------------------- paged key-value cache
+ * The attention half of a layer keeps each request's keys and values in pages
+ * of page_size tokens, which a table [S][W] maps to the request's positions
+ * (position j of request s lies in page table[s][j / page_size] at offset
+ * j % page_size; its slot is page * page_size + offset).  The kwkr.cn Coder
+ * write-up ("测试环境与运行配置") keeps 8-bit keys and values at long contexts,
+ * here e4m3 with one fp32 scale per (token, head): value = scale * element.
+ *   dtype    MOE_BF16 or MOE_FP8_E4M3.
+ *   k        [num_pages][n_kv_heads][head_dim / X][page_size][X], X = 16 bytes
+ *            of elements (8 bf16, 16 e4m3): the layout in which a wave's loads
+ *            of 16 tokens' keys are contiguous.
+ *   v        [num_pages][n_kv_heads][page_size][head_dim].
+ *   k_scale, v_scale [num_pages][n_kv_heads][page_size] fp32 (e4m3; NULL for
+ *            bf16).
+ * k, v and the scales are 16-byte aligned.  page_size is a power of two in
+ * [16, 1024], head_dim 64, 128 or 256, and num_pages * page_size fits int32
+ * (other shapes: MOE_ERR_UNSUPPORTED). */
+typedef struct {
+    int32_t dtype; /* moe_dtype */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+} moe_kv_cache;
+
+/* ---------------------------------------------------------------- page tables and slots
+ * One step's bookkeeping from the requests' lengths, on the GPU.  Request s
+ * has cached_len[s] tokens in the cache and brings new_len[s] more (both
+ * clamped to >= 0); the batch has T rows, requests one after another.
+ *     m_s = min(new_len[s], W * page_size - cached_len[s])
+ *     q_offsets[s] = min(T, sum_{r<s} m_r);  n_s = q_offsets[s+1] - q_offsets[s]
+ *     kv_len[s] = cached_len[s] + n_s          (cached_len clamped to W * page_size)
+ *     have_s = ceil(cached_len[s] / page_size), take_s = ceil(kv_len[s] / page_size) - have_s
+ *     page_table[s][have_s + j] = free_pages[sum_{r<s} take_r + j], j < take_s
+ * (-1 where the list of n_free pages has ended), so tokens that do not fit the
+ * batch or the table are not admitted.  The table's other entries are read,
+ * where a new token falls into a page that is there, and left as they are.
+ *   positions [T] int32 out: row t's position in its request; 0 behind the
+ *             last row q_offsets[S].
+ *   slots     [T] int32 out: its cache slot; -1 behind the last row and where
+ *             the table holds no page (an entry < 0).
+ *   counts    [2] int32 out: the rows in use (q_offsets[S]) and the pages
+ *             needed (sum take_s; more than n_free: the list was too short).
+ * The outputs depend on the inputs alone, so a repeated call gives the same.
+ * Unsupported: S > 4096; page_size not a power of two in [16, 1024]. */
+moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_t S, const int32_t* free_pages,
+                       int32_t n_free, int32_t page_size, int32_t T, int32_t* page_table, int32_t W,
+                       int32_t* q_offsets, int32_t* kv_len, int32_t* positions, int32_t* slots, int32_t* counts,
+                       moe_stream stream);
+
+/* ---------------------------------------------------------------- head norms, rotation, cache write
+ * From the fused projection's rows [q heads | k heads | v heads], in one pass:
+ *     q, k: y = x * rsqrt(mean(x^2) + eps) * weight  (per head; skipped when the weight is NULL)
+ *           then the first rope_dim elements rotated by the row's position:
+ *           (a, b) -> rope_scale * (a cos - b sin, b cos + a sin), angle = position * inv_freq[i]
+ *           pair i = elements (i, i + rope_dim / 2), or (2i, 2i + 1) if interleaved
+ *     v:    as it is
+ * in fp32 (the angle in fp64, so far positions keep their phase), rounded once:
+ * q to bf16 into q_out, k and v into the cache at the row's slot (bf16, or e4m3
+ * of y / scale with scale = max |y| / 448 per token and head; an all-zero head
+ * has scale 0).  Long-context scalings change inv_freq and rope_scale.
+ *   qkv       [T] rows of (n_heads + 2 n_kv_heads) * head_dim bf16, qkv_stride
+ *             elements apart.
+ *   q_weight, k_weight [head_dim] fp32, or NULL; inv_freq [rope_dim / 2] fp32
+ *             (NULL with rope_dim 0).
+ *   positions, slots [T] int32 (moe_kv_plan's).  A row whose slot is negative
+ *             or past the cache is padding: nothing of it is written.
+ *   q_out     [T][n_heads][head_dim] bf16; must not overlap qkv.
+ * Two rows with one slot leave either row's keys and values there.
+ * Unsupported: x_dtype other than MOE_BF16; rope_dim not a multiple of 16;
+ * qkv_stride not a multiple of 8; n_heads + 2 n_kv_heads > 1024. */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout;
+
+moe_status moe_qk_norm_rope(const void* qkv, int32_t x_dtype, int64_t qkv_stride, int32_t T, int32_t n_heads,
+                            const moe_kv_cache* cache, const float* q_weight, const float* k_weight, float eps,
+                            const float* inv_freq, int32_t rope_dim, int32_t rope_layout, float rope_scale,
+                            const int32_t* positions, const int32_t* slots, void* q_out, moe_stream stream);
+
+/* ---------------------------------------------------------------- attention over the paged cache
+ * Row i of request s's n = q_offsets[s+1] - q_offsets[s] rows stands at
+ * position p = kv_len[s] - n + i (its own key and value are in the cache) and
+ * sees the positions j <= p, with window > 0 only those with j > p - window.
+ * Query head h reads key-value head h / (n_heads / n_kv_heads):
+ *     s_j = scale * q . k_j;  softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *     out = sum_j softmax(s)_j v_j       (a row that sees nothing: 0)
+ * The products' operands are bf16 (e4m3 elements are exact in bf16; the scales
+ * enter in fp32, the values' through the probabilities, which are rounded to
+ * bf16 before the second product); scores, maxima, sums and outputs are fp32,
+ * rounded once.  What a row does not see does not reach it, not even as a NaN.
+ *   q, out      [T][n_heads][head_dim] bf16; q's rows q_stride elements apart.
+ *   page_table  [S][W] int32; positions in an entry outside [0, num_pages), and
+ *               those at W * page_size and above, are seen by no row.
+ *   q_offsets   [S+1] ascending in [0, T], kv_len [S] (moe_kv_plan's); rows
+ *               behind q_offsets[S] are left as they were.
+ * Long caches are split over the GPU's compute units and joined by a second
+ * kernel, in a fixed order: the result does not vary from run to run.
+ * Unsupported: q_dtype other than MOE_BF16; S > 4096; n_heads not a multiple of
+ * n_kv_heads, or n_heads / n_kv_heads > 64; q_stride not a multiple of 8. */
+size_t moe_paged_attn_workspace_size(int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t S);
+moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t T, int32_t n_heads,
+                          const moe_kv_cache* cache, const int32_t* page_table, int32_t W, const int32_t* q_offsets,
+                          const int32_t* kv_len, int32_t S, float scale, float softcap, int32_t window, void* out,
+                          void* workspace, size_t ws_bytes, moe_stream stream);
+
+/* ---------------------------------------------------------------- product with epilogue
+ * A layer's dense projections:
+ *     out[t][n] = cast( act( sum_k x[t][k] * w[n][k] + bias[n] ) + residual[t][n] )
+ * fp32 accumulation, bias, activation and residual in fp32, one rounding.
+ *   x        [T] rows of K bf16, x_stride elements apart.
+ *   w        [N][K] bf16 (out x in).   bias [N] fp32 or NULL.
+ *   residual [T][N] in out_dtype, or NULL.   out [T][N], MOE_BF16 or MOE_F32;
+ *            may alias residual (not x).
+ *   act      silu z / (1 + e^-z); gelu z * Phi(z); its tanh form; relu max(z, 0).
+ * Unsupported: x_dtype or w_dtype other than MOE_BF16; K not a multiple of 64;
+ * N or x_stride not a multiple of 8. */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SILU = 1,
+    MOE_ACT_GELU = 2,
+    MOE_ACT_GELU_TANH = 3,
+    MOE_ACT_RELU = 4
+} moe_activation;
+
+size_t moe_linear_workspace_size(int32_t T, int32_t N, int32_t K);
+moe_status moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int32_t w_dtype,
+                      const float* bias, int32_t act, const void* residual, int32_t T, int32_t N, int32_t K, void* out,
+                      int32_t out_dtype, void* workspace, size_t ws_bytes, moe_stream stream);
 
 #ifdef __cplusplus
 }

@@ -14,13 +14,15 @@ import torch
 from . import build as _build
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-F32, BF16, INT4_B32, INT2_B32, INT3_B32 = 0, 1, 2, 3, 4
+F32, BF16, INT4_B32, INT2_B32, INT3_B32, FP8_E4M3 = 0, 1, 2, 3, 4, 5
 _QUANT_BY_BITS = {4: INT4_B32, 3: INT3_B32, 2: INT2_B32}
 
 EXPORTS = ["moe_abi_version", "moe_status_string", "moe_route_workspace_size", "moe_route",
            "moe_permute_workspace_size", "moe_permute", "moe_ffn_workspace_size", "moe_ffn",
            "moe_route_group_workspace_size", "moe_route_group", "moe_route_group_noalloc", "moe_combine", "moe_combine_steer", "moe_layer_workspace_size", "moe_layer", "moe_expert_freq", "moe_profile_workspace_size", "moe_profile_rank",
-           "moe_profile_hits", "moe_strp_size", "moe_strp_write", "moe_strp_read", "moe_profile_remap"]
+           "moe_profile_hits", "moe_strp_size", "moe_strp_write", "moe_strp_read", "moe_profile_remap",
+           "moe_kv_plan", "moe_qk_norm_rope", "moe_paged_attn_workspace_size", "moe_paged_attn",
+           "moe_linear_workspace_size", "moe_linear"]
 
 
 class MoeError(RuntimeError):
@@ -33,6 +35,12 @@ class ExpertWeights(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
                 ("w_down", ctypes.c_void_p), ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p),
                 ("s_down", ctypes.c_void_p)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -100,6 +108,19 @@ def load():
     L.moe_strp_read.argtypes = [vp, sz, vp, vp, vp, vp, i32, vp, i64]
     L.moe_profile_remap.restype = ctypes.c_int
     L.moe_profile_remap.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp]
+    f32, kvp = ctypes.c_float, ctypes.POINTER(KVCacheStruct)
+    L.moe_kv_plan.restype = ctypes.c_int
+    L.moe_kv_plan.argtypes = [vp, vp, i32, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp]
+    L.moe_qk_norm_rope.restype = ctypes.c_int
+    L.moe_qk_norm_rope.argtypes = [vp, i32, i64, i32, i32, kvp, vp, vp, f32, vp, i32, i32, f32, vp, vp, vp, vp]
+    L.moe_paged_attn_workspace_size.restype = sz
+    L.moe_paged_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    L.moe_paged_attn.restype = ctypes.c_int
+    L.moe_paged_attn.argtypes = [vp, i32, i64, i32, i32, kvp, vp, i32, vp, vp, i32, f32, f32, i32, vp, vp, sz, vp]
+    L.moe_linear_workspace_size.restype = sz
+    L.moe_linear_workspace_size.argtypes = [i32, i32, i32]
+    L.moe_linear.restype = ctypes.c_int
+    L.moe_linear.argtypes = [vp, i32, i64, vp, i32, vp, i32, vp, i32, i32, i32, vp, i32, vp, sz, vp]
     _lib = L
     return L
 
@@ -499,3 +520,215 @@ def layer(x, w_router, wg, wu, wd, K: int, bias=None, sg=None, su=None, sd=None,
                           _ptr(residual), _ptr(steer_v), _ptr(out), _ptr(idx), _ptr(w), _ptr(counts), _ptr(offsets),
                           _ptr(perm), _ptr(inv), _ptr(ws), nb, _stream(stream)), "moe_layer")
     return out, dict(idx=idx, w=w, counts=counts, offsets=offsets, perm=perm, inv=inv)
+
+
+# ------------------------------------------------------------------ the attention half of a layer
+_FP8 = torch.float8_e4m3fn
+
+
+def _elsewhere(dev, stream) -> bool:
+    """Whether a call has to switch to its tensors' device or to the given stream first (outputs and
+    workspaces it allocates then belong to that stream)."""
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _on(dev, t, name, dtype=None, shape=None):
+    _need(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t
+
+
+def _rows(t, name, dtype):
+    """A [T][n] tensor whose rows are contiguous (they may lie apart)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class KVCache:
+    """A paged key-value cache over tensors in the library's layout (include/moe.h, moe_kv_cache):
+    k [pages][kv heads][head_dim / X][page size][X], X = 8 (bfloat16) or 16 (float8_e4m3fn),
+    v [pages][kv heads][page size][head_dim], and for float8 the fp32 scales
+    k_scale, v_scale [pages][kv heads][page size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dtype not in (torch.bfloat16, _FP8):
+            raise TypeError(f"a cache holds bfloat16 or float8_e4m3fn, not {k.dtype}")
+        _need(k, "k")
+        if k.dim() != 5 or k.shape[4] != 16 // k.element_size():
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected [pages][kv heads][head_dim / X][page size][X]")
+        pages, heads, chunks, page, x = k.shape
+        dev = k.device
+        _on(dev, v, "v", k.dtype, (pages, heads, page, chunks * x))
+        if (k.dtype == _FP8) != (k_scale is not None) or (k.dtype == _FP8) != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a float8 cache")
+        if k_scale is not None:
+            _on(dev, k_scale, "k_scale", torch.float32, (pages, heads, page))
+            _on(dev, v_scale, "v_scale", torch.float32, (pages, heads, page))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page, heads, chunks * x
+        self.device = dev
+        self.struct = KVCacheStruct(BF16 if k.dtype == torch.bfloat16 else FP8_E4M3, pages, page, heads, chunks * x,
+                                    k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                                    None if v_scale is None else v_scale.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def allocate(cls, num_pages, page_size, n_kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
+        if dtype not in (torch.bfloat16, _FP8):
+            raise TypeError(f"a cache holds bfloat16 or float8_e4m3fn, not {dtype}")
+        x = 8 if dtype == torch.bfloat16 else 16
+        k = torch.empty((num_pages, n_kv_heads, head_dim // x, page_size, x), dtype=dtype, device=device)
+        v = torch.empty((num_pages, n_kv_heads, page_size, head_dim), dtype=dtype, device=device)
+        if dtype == torch.bfloat16:
+            return cls(k, v)
+        s = [torch.empty((num_pages, n_kv_heads, page_size), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(k, v, *s)
+
+
+class KVPlan:
+    """The outputs of kv_plan: q_offsets [S+1], kv_len [S], positions [T], slots [T], counts [2], int32."""
+
+    def __init__(self, q_offsets, kv_len, positions, slots, counts):
+        self.q_offsets, self.kv_len, self.positions, self.slots, self.counts = q_offsets, kv_len, positions, slots, counts
+
+    @classmethod
+    def allocate(cls, S, T, device="cuda"):
+        return cls(*(torch.empty(n, dtype=torch.int32, device=device) for n in (S + 1, S, T, T, 2)))
+
+
+def kv_plan(cached_len, new_len, free_pages, page_table, page_size: int, T: int, out=None, stream=None) -> KVPlan:
+    """One step's page tables and slots from the requests' lengths (moe_kv_plan): new pages are taken from
+    free_pages into page_table [S][W] (in place); out: optional KVPlan to fill."""
+    dev = cached_len.device
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return kv_plan(cached_len, new_len, free_pages, page_table, page_size, T, out=out)
+    i32 = torch.int32
+    _need(cached_len, "cached_len", i32)
+    S, W = page_table.shape
+    _on(dev, cached_len, "cached_len", i32, (S,))
+    _on(dev, new_len, "new_len", i32, (S,))
+    _on(dev, free_pages, "free_pages", i32)
+    _on(dev, page_table, "page_table", i32)
+    p = out if out is not None else KVPlan.allocate(S, T, dev)
+    if out is not None:
+        for n, t, m in (("q_offsets", p.q_offsets, S + 1), ("kv_len", p.kv_len, S), ("positions", p.positions, T),
+                        ("slots", p.slots, T), ("counts", p.counts, 2)):
+            _on(dev, t, n, i32, (m,))
+    _chk(load().moe_kv_plan(_ptr(cached_len), _ptr(new_len), S, _ptr(free_pages), free_pages.numel(), page_size, T,
+                            _ptr(page_table), W, _ptr(p.q_offsets), _ptr(p.kv_len), _ptr(p.positions), _ptr(p.slots),
+                            _ptr(p.counts), _stream()), "moe_kv_plan")
+    return p
+
+
+def qk_norm_rope(qkv, cache: KVCache, positions, slots, q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                 interleaved=False, rope_scale=1.0, out=None, stream=None):
+    """Head norms, rotation and cache write of the fused projection's rows qkv [T][(n_heads + 2 n_kv_heads) *
+    head_dim] (moe_qk_norm_rope).  The rotated part of a head is twice inv_freq's length.  Returns q
+    [T][n_heads][head_dim] (out: optional tensor to fill)."""
+    dev = qkv.device
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return qk_norm_rope(qkv, cache, positions, slots, q_weight, k_weight, eps, inv_freq, interleaved,
+                                rope_scale, out)
+    stride = _rows(qkv, "qkv", torch.bfloat16)
+    T, n = qkv.shape
+    D = cache.head_dim
+    Hq = n // D - 2 * cache.n_kv_heads
+    if n % D or Hq <= 0:
+        raise ValueError(f"qkv rows of {n} elements are not (n_heads + 2 * {cache.n_kv_heads}) heads of {D}")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on {cache.device}, expected {dev}")
+    _on(dev, positions, "positions", torch.int32, (T,))
+    _on(dev, slots, "slots", torch.int32, (T,))
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _on(dev, t, name, torch.float32, (D,))
+    R = 0
+    if inv_freq is not None:
+        R = 2 * _on(dev, inv_freq, "inv_freq", torch.float32).numel()
+    q = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    _on(dev, q, "out", torch.bfloat16, (T, Hq, D))
+    _chk(load().moe_qk_norm_rope(_ptr(qkv), BF16, stride, T, Hq, cache.ref, _ptr(q_weight), _ptr(k_weight), eps,
+                                 _ptr(inv_freq), R, 1 if interleaved else 0, rope_scale, _ptr(positions), _ptr(slots),
+                                 _ptr(q), _stream()), "moe_qk_norm_rope")
+    return q
+
+
+def paged_attention_workspace_size(T, n_heads, n_kv_heads, head_dim, S) -> int:
+    return int(load().moe_paged_attn_workspace_size(T, n_heads, n_kv_heads, head_dim, S))
+
+
+def paged_attention(q, cache: KVCache, page_table, q_offsets, kv_len, scale=None, softcap=0.0, window=0, out=None,
+                    workspace=None, stream=None):
+    """Attention of the rows q [T][n_heads][head_dim] over their requests' cached positions (moe_paged_attn);
+    scale defaults to head_dim ** -0.5.  Rows of q may lie apart.  Returns out [T][n_heads][head_dim]."""
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return paged_attention(q, cache, page_table, q_offsets, kv_len, scale, softcap, window, out, workspace)
+    if q.dim() != 3:
+        raise ValueError("q must be [T][n_heads][head_dim]")
+    T, Hq, D = q.shape
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be torch.bfloat16, not {q.dtype}")
+    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D):
+        raise ValueError("a row of q must be contiguous")
+    if cache.device != dev or cache.head_dim != D:
+        raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}, q has {D} on {dev}")
+    S, W = page_table.shape
+    _on(dev, page_table, "page_table", torch.int32)
+    _on(dev, q_offsets, "q_offsets", torch.int32, (S + 1,))
+    _on(dev, kv_len, "kv_len", torch.int32, (S,))
+    o = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    _on(dev, o, "out", torch.bfloat16, (T, Hq, D))
+    nb = paged_attention_workspace_size(T, Hq, cache.n_kv_heads, D, S)
+    ws = _workspace(nb, dev, workspace)
+    _chk(load().moe_paged_attn(_ptr(q), BF16, q.stride(0) if T > 1 else Hq * D, T, Hq, cache.ref, _ptr(page_table), W,
+                               _ptr(q_offsets), _ptr(kv_len), S, D ** -0.5 if scale is None else scale, softcap,
+                               window, _ptr(o), _ptr(ws), max(nb, 1), _stream()), "moe_paged_attn")
+    return o
+
+
+_ACT = {None: 0, "none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+
+def linear_workspace_size(T, N, K) -> int:
+    return int(load().moe_linear_workspace_size(T, N, K))
+
+
+def linear(x, w, bias=None, act=None, residual=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """act(x w^T + bias) + residual in one rounding (moe_linear): x [T][K] (rows may lie apart) and w [N][K]
+    bfloat16, bias [N] fp32, act None, "silu", "gelu", "gelu_tanh" or "relu", residual [T][N] in the output's
+    dtype (bfloat16 or float32; out may be the residual)."""
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return linear(x, w, bias, act, residual, out_dtype, out, workspace)
+    stride = _rows(x, "x", torch.bfloat16)
+    T, K = x.shape
+    N = w.shape[0]
+    _on(dev, w, "w", torch.bfloat16, (N, K))
+    if act not in _ACT:
+        raise ValueError(f"unknown activation {act!r}")
+    if bias is not None:
+        _on(dev, bias, "bias", torch.float32, (N,))
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
+    if residual is not None:
+        _on(dev, residual, "residual", out_dtype, (T, N))
+    o = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=dev)
+    _on(dev, o, "out", out_dtype, (T, N))
+    nb = linear_workspace_size(T, N, K)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    _chk(load().moe_linear(_ptr(x), BF16, stride, _ptr(w), BF16, _ptr(bias), _ACT[act], _ptr(residual), T, N, K,
+                           _ptr(o), _act_dtype(o), _ptr(ws), nb, _stream()), "moe_linear")
+    return o

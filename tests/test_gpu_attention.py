@@ -1,0 +1,375 @@
+"""GPU: the attention half (page tables and slots, head norms + rotation + cache
+write, paged attention, dense products) against plain 64-bit forms, at the
+sizes and masks where each can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from routed_expert_ffn_amd import moe
+
+from . import attn_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF, FP8 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    moe.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def rng(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def ints(v):
+    return torch.tensor(np.asarray(v, np.int32).reshape(-1)).cuda()
+
+
+# ---------------------------------------------------------------- page tables and slots
+PLANS = [
+    # (cached, new, free pages, table width, page size, rows)
+    ([0], [1], 3, 4, 16, 1),
+    ([0], [0], 0, 1, 16, 0),
+    ([15, 16, 17, 0, 31], [1, 1, 1, 5, 2], 9, 4, 16, 10),
+    ([5, 0, 100], [3, 0, 60], 9, 16, 16, 80),                      # a padded batch
+    ([5, 0, 100], [3, 40, 60], 9, 16, 16, 50),                     # rows run out inside the last request
+    ([5, 0, 100], [3, 40, 60], 2, 16, 16, 120),                    # pages run out
+    ([60, 64, 70, -3], [10, 9, 8, -1], 9, 4, 16, 40),              # the table is full, lengths past it, negative ones
+    ([7] * 300, [1, 2, 3] * 100, 700, 3, 16, 640),                 # more requests than threads of a block
+    (list(range(0, 2100)), [2] * 2100, 300, 70, 32, 4300),
+    ([1023] * 4096, [2, 0] * 2048, 3000, 3, 1024, 4100),           # the most requests, the largest page
+]
+
+
+@pytest.mark.parametrize("case", range(len(PLANS)))
+def test_kv_plan(case):
+    cached, new, n_free, W, page, T = PLANS[case]
+    g = np.random.default_rng(case)
+    S = len(cached)
+    table = g.permutation(S * W).reshape(S, W).astype(np.int32)
+    if case == 3:
+        table[2, 6] = -1                                           # a page that is not there
+    free = g.permutation(5000)[:n_free].astype(np.int32)
+    want = ref.plan(cached, new, free, table, page, T)
+    dt = torch.from_numpy(table).cuda()
+    for _ in range(2):                                             # a repeated call gives the same
+        p = moe.kv_plan(ints(cached), ints(new), ints(free), dt, page, T)
+        torch.cuda.synchronize()
+        for name, t, w in zip(("q_offsets", "kv_len", "positions", "slots", "counts", "table"),
+                              (p.q_offsets, p.kv_len, p.positions, p.slots, p.counts, dt), want):
+            assert np.array_equal(t.cpu().numpy(), w), name
+
+
+# ---------------------------------------------------------------- norms, rotation, cache write
+ROPES = [
+    # T, Hq, Hkv, D, rope_dim, interleaved, fp8, norm, page, first position, rope_scale
+    (1, 1, 1, 64, 64, False, False, True, 16, 0, 1.0),
+    (5, 16, 2, 256, 64, False, False, True, 16, 30000, 1.0),
+    (5, 16, 2, 256, 64, True, True, True, 16, 30000, 1.0),
+    (3, 8, 8, 128, 128, True, False, True, 64, 262000, 1.25),
+    (3, 6, 2, 128, 128, False, True, False, 32, 7, 1.0),
+    (4, 5, 1, 64, 16, False, True, True, 16, 1 << 30, 1.0),
+    (7, 3, 3, 64, 0, False, False, True, 16, 3, 1.0),               # no rotation
+    (2, 2, 1, 256, 256, False, False, False, 1024, 100, 1.0),       # no norm
+    (300, 4, 2, 128, 96, False, True, True, 16, 5000, 1.1),         # many rows: 16 per block
+    (259, 7, 1, 64, 32, True, False, True, 16, 11, 1.0),
+    (273, 3, 2, 256, 256, False, False, True, 32, 9, 1.0),
+]
+
+
+def rope_inputs(case):
+    T, Hq, Hkv, D, R, inter, fp8, norm, page, start, mscale = case
+    g = rng(T * 1000 + D)
+    n = Hq + 2 * Hkv
+    qkv = (torch.randn(T, n * D, generator=g) * torch.exp(torch.randn(T, 1, generator=g))).to(BF)
+    if T > 2:
+        qkv.view(T, n, D)[1, -1] = 0                                # a head of zeros
+    pages = -(-T // page) + 2
+    order = torch.randperm(pages * page, generator=g)[:T].to(torch.int32)
+    if T > 3:
+        order[T // 2] = -1                                          # padding rows
+        order[T - 1] = pages * page
+    pos = torch.arange(start, start + T, dtype=torch.int64).to(torch.int32)
+    freq = (10000.0 ** (-torch.arange(0, R, 2).double() / max(R, 1))).float() if R else None
+    qw = (1 + 0.2 * torch.randn(D, generator=g)) if norm else None
+    kw = (1 + 0.2 * torch.randn(D, generator=g)) if norm else None
+    return qkv, pages, order, pos, freq, qw, kw
+
+
+@pytest.mark.parametrize("case", ROPES, ids=lambda c: "-".join(map(str, c)))
+def test_qk_norm_rope(case):
+    T, Hq, Hkv, D, R, inter, fp8, norm, page, start, mscale = case
+    qkv, pages, slots, pos, freq, qw, kw = rope_inputs(case)
+    want, size = ref.qk_norm_rope(qkv, Hq, Hkv, D, pos, qw, kw, 1e-5, freq, inter, mscale)
+    slack = ref.norm_rope_slack(size, D)
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cache = moe.KVCache.allocate(pages, page, Hkv, D, FP8 if fp8 else BF)
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8).fill_(0x41)
+    if fp8:
+        cache.k_scale.fill_(7.0)
+        cache.v_scale.fill_(7.0)
+    q = torch.full((T, Hq, D), 9.0, dtype=BF, device="cuda")
+    wide = torch.full((T, qkv.shape[1] + 40), math.nan, dtype=BF, device="cuda")      # rows that lie apart
+    wide[:, :qkv.shape[1]] = qkv.cuda()
+    moe.qk_norm_rope(wide[:, :qkv.shape[1]], cache, dev(pos), dev(slots), dev(qw), dev(kw), 1e-5, dev(freq), inter,
+                     mscale, out=q)
+    torch.cuda.synchronize()
+    real = (slots >= 0) & (slots < pages * page)
+    got = q.cpu().double()
+    assert bool((got[~real] == 9.0).all()), "a padding row's output was written"
+    bound = ref.BF16_HALF * want[:, :Hq].abs() + 1.01 * slack[:, :Hq]
+    assert bool(((got - want[:, :Hq]).abs() <= bound)[real].all())
+    at = slots[real].long()
+    untouched = torch.ones(pages * page, dtype=torch.bool)
+    untouched[at] = False
+    for name, t, sc, h0 in (("k", cache.k, cache.k_scale, Hq), ("v", cache.v, cache.v_scale, Hq + Hkv)):
+        raw = t.cpu()
+        rows = ref.k_rows(raw.view(torch.uint8) if fp8 else raw) if name == "k" else (raw.view(torch.uint8) if fp8 else raw)
+        rows = rows.transpose(1, 2).reshape(pages * page, Hkv, D)
+        flat = rows if fp8 else rows.contiguous().view(torch.uint8)
+        assert bool((flat[untouched] == 0x41).all()), f"{name}: another slot was written"
+        y, e = want[real][:, h0:h0 + Hkv], slack[real][:, h0:h0 + Hkv]
+        if name == "v":
+            e = e * 0
+        if not fp8:
+            assert bool(((rows[at].double() - y).abs() <= ref.BF16_HALF * y.abs() + 1.01 * e).all()), name
+        else:
+            s = sc.cpu().transpose(1, 2).reshape(pages * page, Hkv)
+            assert bool((s[untouched] == 7.0).all())
+            s = s[at].double()
+            amax = y.abs().amax(-1)
+            assert bool(((s - amax / 448).abs() <= 1.01 * e.amax(-1) / 448 + 2 * ref.F32_HALF * s).all())
+            val = rows[at].contiguous().view(FP8).float().double() * s[..., None]
+            # half a step of e4m3: relative 2^-4, at least half of 2^-9 (its subnormal step) of the scale; the scale's
+            # own error moves the element by the same share
+            tol = torch.maximum(ref.FP8_HALF * y.abs(), 2.0 ** -10 * s[..., None]) + 1.2 * e + 4 * ref.F32_HALF * y.abs() \
+                + 1.2 * (e.amax(-1) / torch.clamp(amax, min=1e-30))[..., None] * y.abs()
+            assert bool(((val - y).abs() <= tol).all()), name
+
+
+# ---------------------------------------------------------------- paged attention
+def attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=0, pad=0, W=None, spare=3, poison=True):
+    """q, a cache whose unused places hold NaN, a page table whose unused entries are garbage."""
+    g = rng(seed)
+    S = len(lens)
+    W = W or max(1, max(-(-n // page) for n in lens)) + 1
+    used = [min(-(-n // page), W) for n in lens]
+    pages = sum(used) + spare
+    order = torch.randperm(pages, generator=g)
+    table = torch.full((S, W), 0x7FFFFFF0, dtype=torch.int32)
+    k = torch.full((pages, Hkv, page, D), math.nan if poison else 0.0)
+    v = torch.full((pages, Hkv, page, D), math.nan if poison else 0.0)
+    at = 0
+    for s in range(S):
+        for j in range(used[s]):
+            p = int(order[at])
+            at += 1
+            table[s, j] = p
+            m = min(page, lens[s] - j * page)
+            k[p, :, :m] = torch.randn(Hkv, m, D, generator=g) + 0.5
+            v[p, :, :m] = torch.randn(Hkv, m, D, generator=g) * 2
+    T = sum(new) + pad
+    q = torch.randn(T, Hq, D, generator=g).to(BF)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    ks = vs = None
+    if fp8:
+        ks, vs = k.abs().amax(-1) / 448, v.abs().amax(-1) / 448
+        k, v = (k / ks[..., None]).to(FP8), (v / vs[..., None]).to(FP8)
+        kl = ref.k_layout(k.view(torch.uint8), 16).view(FP8)
+    else:
+        k, v = k.to(BF), v.to(BF)
+        kl = ref.k_layout(k, 8)
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    cache = moe.KVCache(dev(kl), dev(v.contiguous()), dev(ks), dev(vs))
+    return dict(q=q, k=ref.as_values(k, ks), v=ref.as_values(v, vs), table=table, offs=offs, lens=np.array(lens, np.int32),
+                cache=cache, page=page, D=D, T=T, rows=int(sum(new)))
+
+
+def run_attn(st, scale=None, softcap=0.0, window=0, q=None, table=None):
+    out = torch.full(st["q"].shape, 5.0, dtype=BF, device="cuda")
+    moe.paged_attention(st["q"].cuda() if q is None else q, st["cache"],
+                        (st["table"] if table is None else table).cuda(), ints(st["offs"]), ints(st["lens"]),
+                        scale=scale, softcap=softcap, window=window, out=out)
+    torch.cuda.synchronize()
+    return out.cpu()
+
+
+def check_attn(st, got, scale=None, softcap=0.0, window=0, table=None, v=None):
+    scale = st["D"] ** -0.5 if scale is None else scale
+    want, mass, reach = ref.attention(st["q"], st["k"], st["v"] if v is None else v,
+                                      st["table"] if table is None else table, st["offs"], st["lens"], st["page"],
+                                      scale, softcap, window)
+    n = st["rows"]
+    assert bool((got[n:] == 5.0).all()), "a row behind the last request was written"
+    bound = ref.attention_bound(want, mass, reach, st["D"], int(max(st["lens"], default=1)))[:n]
+    err = (got[:n].double() - want[:n]).abs()
+    bad = ~(err <= bound)
+    assert not bool(bad.any()), f"{int(bad.sum())} values off, worst {float((err - bound).max())} at {bad.nonzero()[0].tolist()}"
+
+
+ATTNS = [
+    # lens, new, Hq, Hkv, D, page, fp8, window, softcap
+    ([1], [1], 1, 1, 64, 16, False, 0, 0.0),
+    ([1], [1], 8, 1, 128, 16, True, 0, 0.0),
+    ([33], [1], 16, 2, 256, 16, False, 0, 0.0),
+    ([130], [5], 16, 2, 256, 16, True, 0, 0.0),
+    ([16, 17, 31, 32, 33, 127, 128, 129], [1] * 8, 4, 2, 128, 16, False, 0, 0.0),
+    ([257, 3, 64, 700], [1, 3, 5, 8], 8, 2, 128, 64, False, 0, 0.0),
+    ([257, 3, 64, 700], [2, 3, 0, 8], 8, 2, 64, 32, True, 0, 30.0),
+    ([300, 200], [40, 33], 8, 2, 128, 16, False, 0, 0.0),            # three and more row tiles
+    ([300, 200], [40, 33], 6, 1, 64, 16, False, 70, 0.0),            # a group of 6
+    ([90], [50], 3, 3, 64, 16, True, 20, 20.0),
+    ([1500, 40], [4, 4], 4, 1, 128, 128, False, 100, 0.0),           # a window that leaves most pages out
+    ([1500, 700], [1, 1], 2, 2, 256, 1024, False, 0, 0.0),
+    ([5000], [1], 4, 1, 64, 16, False, 0, 0.0),                      # many splits
+    ([3000, 10], [7, 7], 2, 1, 128, 32, True, 0, 0.0),
+    ([5], [1], 64, 1, 64, 16, False, 0, 0.0),                        # the largest group
+]
+
+
+@pytest.mark.parametrize("case", ATTNS, ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_paged_attention(case):
+    lens, new, Hq, Hkv, D, page, fp8, window, cap = case
+    st = attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=sum(lens), pad=2)
+    check_attn(st, run_attn(st, softcap=cap, window=window), softcap=cap, window=window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_attention_rows_that_see_nothing(fp8):
+    # no cached position at all; more rows than positions; pages outside the cache
+    st = attn_state([0, 2, 40, 50], [1, 5, 1, 2], 4, 2, 64, 16, fp8, seed=3)
+    table = st["table"].clone()
+    table[2] = -1                                    # request 2 has no page
+    table[3, 1] = st["cache"].num_pages              # request 3 lacks positions 16..31
+    got = run_attn(st, table=table)
+    check_attn(st, got, table=table)
+    assert bool((got[0] == 0).all()) and bool((got[1:4] == 0).all()) and bool((got[6] == 0).all())
+
+
+def test_paged_attention_lengths_past_the_table():
+    st = attn_state([100], [2], 2, 1, 64, 16, False, seed=4, W=4)    # 64 positions fit
+    check_attn(st, run_attn(st))
+
+
+@pytest.mark.parametrize("D,fp8", [(64, False), (128, False), (128, True), (256, False)])
+def test_paged_attention_unseen_infinities_do_not_reach_a_row(D, fp8):
+    # the newest tokens' values and keys are infinite or NaN: the rows before them do not see them
+    st = attn_state([70], [6], 4, 2, D, 16, fp8, seed=5)
+    page, off = int(st["table"][0, 67 // 16]), 67 % 16
+    bad = math.nan if fp8 else math.inf
+    if fp8:
+        st["cache"].v.view(torch.uint8)[page, :, off, 3] = 0x7F
+    else:
+        st["cache"].v[page, :, off, 3] = math.inf
+        st["cache"].v[page, 0, off, 5] = -math.inf
+        st["v"][page, 0, off, 5] = -math.inf
+    st["v"][page, :, off, 3] = bad
+    got = run_attn(st)
+    n = 3                                             # rows of positions 64, 65, 66
+    want, mass, reach = ref.attention(st["q"], st["k"], st["v"], st["table"], st["offs"], st["lens"], 16, D ** -0.5,
+                                      0.0, 0)
+    bound = ref.attention_bound(want, mass, reach, D, 70)
+    assert bool(((got[:n].double() - want[:n]).abs() <= bound[:n]).all())
+    tail = got[n:].double()
+    assert bool(torch.isnan(tail[:, :, 3]).all()) if fp8 else bool((tail[:, :, 3] == math.inf).all())
+    if not fp8:
+        assert bool((tail[:, :2, 5] == -math.inf).all())
+    rest = [d for d in range(D) if d not in (3, 5)]
+    assert bool(((tail - want[n:]).abs() <= bound[n:])[:, :, rest].all())
+
+
+def test_paged_attention_nan_and_infinite_scores():
+    # a NaN in one head's query, an infinite key: only the rows that meet them are NaN, as in the formula
+    st = attn_state([40], [3], 4, 2, 64, 16, False, seed=6)
+    st["q"][1, 2, 7] = math.nan
+    got = run_attn(st)
+    assert bool(torch.isnan(got[1, 2]).all())
+    rest = torch.ones(3, 4, dtype=torch.bool)
+    rest[1, 2] = False
+    assert bool(torch.isfinite(got[rest]).all())
+
+
+def test_paged_attention_strided_queries_and_scale():
+    st = attn_state([77, 130], [2, 1], 4, 2, 128, 16, False, seed=7)
+    wide = torch.full((3, 4 * 128 + 64), math.nan, dtype=BF, device="cuda")
+    wide[:, :512] = st["q"].view(3, 512).cuda()
+    check_attn(st, run_attn(st, scale=0.2, q=wide[:, :512].view(3, 4, 128)), scale=0.2)
+
+
+def test_paged_attention_shared_pages_and_repeats_are_identical():
+    # two requests that share every page; the same call twice gives the same bits, also with many splits
+    st = attn_state([4000, 4000], [1, 1], 8, 1, 128, 16, False, seed=8)
+    st["table"][1] = st["table"][0]
+    st["q"][1] = st["q"][0]
+    a, b = run_attn(st), run_attn(st)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert torch.equal(a[0].view(torch.int16), a[1].view(torch.int16))
+    st["k"], st["v"] = st["k"].nan_to_num(), st["v"].nan_to_num()
+    check_attn(st, a)
+
+
+# ---------------------------------------------------------------- dense products
+LINEARS = [
+    # T, N, K, act, bias, residual, out dtype
+    (1, 8, 64, None, False, False, BF),
+    (1, 1000, 128, "silu", True, True, BF),
+    (5, 2560, 2048, None, False, False, BF),
+    (8, 520, 1088, "gelu", True, False, torch.float32),
+    (16, 264, 512, "relu", True, True, BF),
+    (17, 72, 192, "gelu_tanh", False, True, torch.float32),
+    (33, 200, 256, "silu", False, False, BF),
+    (64, 2048, 320, None, True, True, BF),
+    (130, 136, 640, "gelu_tanh", True, True, torch.float32),
+    (257, 512, 64, None, False, True, BF),
+    (300, 1032, 128, "gelu", True, False, BF),
+    (513, 768, 1024, None, False, True, torch.float32),
+    (1100, 520, 192, "silu", True, True, BF),
+]
+
+
+@pytest.mark.parametrize("case", LINEARS, ids=lambda c: "-".join(map(str, c)).replace("torch.", ""))
+def test_linear(case):
+    T, N, K, act, bias, residual, dt = case
+    g = rng(T * N + K)
+    x = torch.randn(T, K, generator=g).to(BF)
+    w = (torch.randn(N, K, generator=g) * K ** -0.5).to(BF)
+    b = torch.randn(N, generator=g) if bias else None
+    r = torch.randn(T, N, generator=g).to(dt) if residual else None
+    want, size, y = ref.linear(x, w, b, act, r)
+    wide = torch.full((T, K + 24), math.nan, dtype=BF, device="cuda")
+    wide[:, :K] = x.cuda()
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    bound = ref.linear_bound(want, size, y, K, dt)
+    for xx in (wide[:, :K], x.cuda()):
+        got = moe.linear(xx, dev(w), bias=dev(b), act=act, residual=dev(r), out_dtype=dt)
+        assert got.dtype == dt and bool(((got.cpu().double() - want).abs() <= bound).all())
+    if residual:                                     # in place on the residual stream
+        rr = dev(r)
+        assert moe.linear(x.cuda(), dev(w), bias=dev(b), act=act, residual=rr, out=rr) is rr
+        assert bool(((rr.cpu().double() - want).abs() <= bound).all())
+
+
+def test_linear_writes_its_output_only():
+    T, N, K = 37, 72, 128
+    buf = torch.full((T + 2, N), 3.0, dtype=BF, device="cuda")
+    moe.linear(torch.randn(T, K, device="cuda").to(BF), torch.randn(N, K, device="cuda").to(BF), out=buf[1:-1])
+    torch.cuda.synchronize()
+    assert bool((buf[0] == 3.0).all()) and bool((buf[-1] == 3.0).all())
+
+
+def test_linear_infinities_stay_in_their_row_and_column():
+    T, N, K = 20, 40, 128
+    x, w = torch.randn(T, K), torch.randn(N, K)
+    x[3, 5], w[7, 9] = math.nan, math.inf
+    got = moe.linear(x.to(BF).cuda(), w.to(BF).cuda()).cpu()
+    fine = torch.isfinite(got)
+    want = torch.ones(T, N, dtype=torch.bool)
+    want[3], want[:, 7] = False, False
+    assert torch.equal(fine, want)
