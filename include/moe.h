@@ -371,7 +371,8 @@ typedef struct {
  *   counts    [2] int32 out: the rows in use (q_offsets[S]) and the pages
  *             needed (sum take_s; more than n_free: the list was too short).
  * The outputs depend on the inputs alone, so a repeated call gives the same.
- * Unsupported: S > 4096; page_size not a power of two in [16, 1024]. */
+ * Unsupported: S > 4096; page_size not a power of two in [16, 1024];
+ * W * page_size > 2^30. */
 moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_t S, const int32_t* free_pages,
                        int32_t n_free, int32_t page_size, int32_t T, int32_t* page_table, int32_t W,
                        int32_t* q_offsets, int32_t* kv_len, int32_t* positions, int32_t* slots, int32_t* counts,
@@ -386,8 +387,8 @@ moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_
  *     v:    as it is
  * in fp32 (the angle in fp64, so far positions keep their phase), rounded once:
  * q to bf16 into q_out, k and v into the cache at the row's slot (bf16, or e4m3
- * of y / scale with scale = max |y| / 448 per token and head; an all-zero head
- * has scale 0).  Long-context scalings change inv_freq and rope_scale.
+ * of 448 y / max |y| with the scale max |y| / 448 per token and head; a head of
+ * zeros, or of values below 2^-117, is stored as zeros of scale 0).  Long-context scalings change inv_freq and rope_scale.
  *   qkv       [T] rows of (n_heads + 2 n_kv_heads) * head_dim bf16, qkv_stride
  *             elements apart.
  *   q_weight, k_weight [head_dim] fp32, or NULL; inv_freq [rope_dim / 2] fp32
@@ -424,7 +425,8 @@ moe_status moe_qk_norm_rope(const void* qkv, int32_t x_dtype, int64_t qkv_stride
  * Long caches are split over the GPU's compute units and joined by a second
  * kernel, in a fixed order: the result does not vary from run to run.
  * Unsupported: q_dtype other than MOE_BF16; S > 4096; n_heads not a multiple of
- * n_kv_heads, or n_heads / n_kv_heads > 64; q_stride not a multiple of 8. */
+ * n_kv_heads, or n_heads / n_kv_heads > 64; q_stride not a multiple of 8;
+ * W * page_size > 2^30. */
 size_t moe_paged_attn_workspace_size(int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t S);
 moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t T, int32_t n_heads,
                           const moe_kv_cache* cache, const int32_t* page_table, int32_t W, const int32_t* q_offsets,

@@ -48,7 +48,7 @@ moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_
         (T > 0 && (!positions || !slots)))
         return MOE_ERR_INVALID_ARG;
     const int shift = page_shift_of(page_size);
-    if (shift < 0 || S_ > MAX_REQUESTS || (int64_t)W * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (shift < 0 || S_ > MAX_REQUESTS || (int64_t)W * page_size > ((int64_t)1 << 30)) return MOE_ERR_UNSUPPORTED;
     if (!aligned4(cached_len) || !aligned4(new_len) || !aligned4(free_pages) || !aligned4(page_table) ||
         !aligned4(q_offsets) || !aligned4(kv_len) || !aligned4(positions) || !aligned4(slots) || !aligned4(counts))
         return MOE_ERR_UNSUPPORTED;
@@ -96,7 +96,7 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
     if (!page_table || !q_offsets || !kv_len || (T > 0 && (!q || !out))) return MOE_ERR_INVALID_ARG;
     if (q_stride < (int64_t)n_heads * kv.head_dim || (int64_t)T * n_heads > INT32_MAX) return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_BF16 || S_ > MAX_REQUESTS || n_heads % kv.n_kv_heads != 0 ||
-        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)W * (1 << kv.page_shift) > INT32_MAX)
+        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
         return MOE_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !aligned4(page_table) || !aligned4(q_offsets) || !aligned4(kv_len))
         return MOE_ERR_UNSUPPORTED;

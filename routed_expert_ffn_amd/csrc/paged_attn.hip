@@ -19,11 +19,15 @@
 // a whole row; MFMA m of the second product then takes element E r + m as its
 // row r, and one byte permute per register pairs up two positions' elements.
 // One pass with a running maximum and sum per row, both in registers; the
-// waves of a block take the tiles in turn and are joined through LDS, the
-// splits of a request by k_attn_join.
+// waves of a block take the tiles in turn and are joined through LDS.
 //
-// Bound by HBM at few rows (each cached byte is used for 16 rows at a time):
-// see launch_paged_attn for how the work is split.
+// The work, for a balanced load whatever the lengths: a unit is (request, row
+// group, key-value head), its length in steps of 32 NW positions; all units'
+// steps in a row are cut into equal shares, one per block.  A block walks the
+// pieces of units in its share; a unit that lies in several shares leaves a
+// partial result in each, which k_attn_join adds up in the order of the shares.
+//
+// Bound by HBM at few rows: each cached byte is used for 16 MT rows at a time.
 #include "attn.h"
 #include "common.h"
 #include "device.h"
@@ -33,12 +37,12 @@ namespace {
 
 constexpr int NW = 4;                       // waves per block
 constexpr int AT_THREADS = NW * WAVE;
-constexpr int TILE = 32;                    // positions per wave step
 constexpr float LOG2E = 1.44269504088896341f;
 
 typedef uint32_t u32x2_a __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_a __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_a __attribute__((ext_vector_type(2)));
+typedef short s16x4_a __attribute__((ext_vector_type(4)));
 
 MOE_DEV uint32_t pk_bf16(float lo, float hi) {
     const bf16x2_a v = {(__bf16)lo, (__bf16)hi};
@@ -48,6 +52,11 @@ MOE_DEV uint32_t pk_bf16(float lo, float hi) {
 template <bool HI>
 MOE_DEV uint32_t fp8x2_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+MOE_DEV int64_t wave_sum64(int64_t v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, WAVE);
+    return v;
 }
 
 struct AttnArgs {
@@ -63,20 +72,21 @@ struct AttnArgs {
     float scale, softcap;
     int window;
     uint16_t* out;
-    int target;                             // items the splitting aims at (grid blocks)
-    int4* meta;                             // [S] (first partial, splits, 0, 0)
-    float* part;                            // [partial][rows][D] unnormalised sums
-    float2* ml;                             // [partial][rows] (maximum, sum)
+    int shares;                             // blocks of the attention launch
+    int64_t* share;                         // [1] steps per share, written by block 0 for the join
+    int64_t* base;                          // [S] first step of each request
+    float* part;                            // [2 shares][rows][D] unnormalised sums
+    float2* ml;                             // [2 shares][rows] (maximum, sum)
 };
 
-// What a block needs of a request: its row range, positions and split.
+// What a block needs of a request: its row range, positions and units.
 struct Request {
     int row0, n, first;                     // first batch row, rows, position of its first row
     int len;                                // positions that the table can hold
-    int range;                              // positions that any of its rows may see
-    int groups;                             // items per key-value head and split
+    int units;                              // row groups * key-value heads
+    int steps;                              // steps of each of its units
 };
-MOE_DEV Request request_of(const AttnArgs& a, int s, int rows_per_item) {
+MOE_DEV Request request_of(const AttnArgs& a, int s, int rows_per_unit, int step_len) {
     Request r;
     const int b = min(max(a.q_offsets[s], 0), a.T), e = min(max(a.q_offsets[s + 1], 0), a.T);
     const int L = max(a.kv_len[s], 0);
@@ -85,172 +95,280 @@ MOE_DEV Request request_of(const AttnArgs& a, int s, int rows_per_item) {
     r.first = L - r.n;
     r.len = (int)min((int64_t)L, (int64_t)a.W << a.kv.page_shift);
     const int lo = a.window > 0 ? max(r.first - a.window + 1, 0) : 0;
-    r.range = max(r.len - lo, 0);
     const int G = a.n_heads / a.kv.n_kv_heads;
-    r.groups = (int)(((int64_t)r.n * G + rows_per_item - 1) / rows_per_item);
+    r.units = (int)(((int64_t)r.n * G + rows_per_unit - 1) / rows_per_unit) * a.kv.n_kv_heads;
+    r.steps = max((int)(((int64_t)max(r.len - lo, 0) + step_len - 1) / step_len), 1);
     return r;
 }
 
-template <int D, int F8>
-struct Tile {                               // one wave's 32 positions
+// One wave's NSUB sub-tiles of 16 positions.
+template <int D, int F8, int NSUB>
+struct Tile {
     static constexpr int KV = F8 ? D / 64 : D / 32;       // 16-byte key chunks per lane and sub-tile
     static constexpr int E = D == 64 ? 4 : 8;             // value elements per lane and load
     static constexpr int NH = D / (16 * E);               // loads per position
     static constexpr int EW = F8 ? E / 4 : E / 2;         // their 32-bit words
-    u32x4_a k[2][KV];
-    uint32_t v[8][NH][EW];
-    f32x4_t ks[2], vs[2];
+    u32x4_a k[NSUB][KV];
+    uint32_t v[4 * NSUB][NH][EW];
+    f32x4_t ks[NSUB], vs[NSUB];
+};
+
+// Buffer loads: a wave-uniform base, a byte offset per lane; `bytes` 0 makes
+// every load return 0 without touching memory.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+MOE_DEV rsrc_t buffer_of(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
+}
+MOE_DEV u32x4_a buf128(rsrc_t r, int off) { return __builtin_bit_cast(u32x4_a, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)); }
+MOE_DEV u32x2_a buf64(rsrc_t r, int off) { return __builtin_bit_cast(u32x2_a, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0)); }
+MOE_DEV uint32_t buf32(rsrc_t r, int off) { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
+
+// the page table through the scalar cache (nothing writes it while the kernel runs)
+typedef const __attribute__((address_space(4))) int32_t* table_ptr;
+
+// blocks per CU, by registers
+constexpr int blocks_per_cu(int D, int MT) { return MT == 1 || (D == 64 && MT == 2) ? 2 : 1; }
+constexpr int shares_of(int D, int MT) { return 256 * blocks_per_cu(D, MT); }
+
+// A kernel's shape: row tiles, sub-tiles per wave step, blocks per CU.
+template <int D, int F8, int MT>
+struct Shape {
+    // 16 KB of cache in flight per wave (8 KB of e4m3), by registers
+    static constexpr int NSUB = D == 256 && (MT > 1 || !F8) ? 1 : 2;
+    static constexpr bool QREG = D * MT <= 128;     // q fragments in registers (up to 16 of them), else LDS at each use
 };
 
 template <int D, int F8, int MT>
-__global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
-    using TL = Tile<D, F8>;
+__global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_attn(const AttnArgs a) {
+    constexpr int NSUB = Shape<D, F8, MT>::NSUB;
+    constexpr bool QREG = Shape<D, F8, MT>::QREG;
+    using TL = Tile<D, F8, NSUB>;
     constexpr int E = TL::E, NH = TL::NH, EW = TL::EW, KV = TL::KV;
-    constexpr int RB = 16 * MT;             // rows per item
-    constexpr bool QREG = D * MT <= 256;    // q fragments in registers (up to 32 of them), else from LDS at each use
+    constexpr int TILE = 16 * NSUB;         // positions per wave step
+    constexpr int STEP = TILE * NW;
+    constexpr int RB = 16 * MT;             // rows per unit
     constexpr int DP = D + 4;               // padded row of the join area
     constexpr int QP = D + 8;               // padded q row, bf16
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    // [S + 1] first item of each request, [S] first partial; then the q rows /
-    // join area; the scan's scratch
-    int* istart = (int*)smem;
-    int* pstart = istart + a.S + 1;
-    unsigned char* area = smem + ((size_t)(2 * a.S + 1) * 4 + 15) / 16 * 16;
+    // more than 64 requests: [S + 1] first steps; then the q rows / join area
+    const bool lanes = a.S <= WAVE;
+    int64_t* base = (int64_t*)smem;
+    unsigned char* area = smem + (lanes ? 0 : ((size_t)(a.S + 1) * 8 + 15) / 16 * 16);
     uint16_t* qs = (uint16_t*)area;                              // [RB][QP]
     float* ja = (float*)area;                                    // [NW][16][DP]
     float2* jml = (float2*)(area + sizeof(float) * NW * 16 * DP);  // [NW][16]
     __shared__ int64_t sc64[NW];
-    __shared__ int sc32[2][NW];
-    __shared__ int strange;                 // the item met infinite or NaN values in a tile seen in part
+    __shared__ int strange;                 // the piece met infinite or NaN values in a tile seen in part
 
     const int tid = threadIdx.x, l = lane_id(), w = __builtin_amdgcn_readfirstlane(tid / WAVE);
     const int G = a.n_heads / a.kv.n_kv_heads, nkv = a.kv.n_kv_heads;
 
-    // ---- the split, from the lengths: U = positions to go over, summed over
-    // row groups and heads; C positions per item so that about `target` items
-    // result, a multiple of the block's 128 positions
-    int64_t U = 0;
-    int RG = 0;
-    for (int s = tid; s < a.S; s += AT_THREADS) {
-        const Request r = request_of(a, s, RB);
-        U += (int64_t)r.groups * nkv * r.range;
-        RG += r.groups * nkv;
-    }
+    // ---- first step of every request.  Up to 64 requests: lane s holds request
+    // s, in every wave by itself.  More: running sums through LDS, 256 at a time.
+    Request mine;
+    int64_t my_base = 0, total;
+    if (lanes) {
+        mine = request_of(a, min(l, a.S - 1), RB, STEP);
+        if (l >= a.S) mine.units = 0;
+        const int64_t c = (int64_t)mine.units * mine.steps;
+        int64_t incl = c;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        U += __shfl_xor(U, d, WAVE);
-        RG += __shfl_xor(RG, d, WAVE);
-    }
-    if (l == 0) { sc64[w] = U; sc32[0][w] = RG; }
-    __syncthreads();
-    U = 0; RG = 0;
-#pragma unroll
-    for (int i = 0; i < NW; i++) { U += sc64[i]; RG += sc32[0][i]; }
-    const int64_t room = RG < a.target / 2 ? a.target - RG : a.target;
-    const int64_t C0 = (U + room - 1) / room;
-    const int64_t C = max((C0 + TILE * NW - 1) / (TILE * NW), (int64_t)1) * (TILE * NW);
-    // first item and first partial of every request: running sums over the
-    // requests, 256 at a time
-    int ibase = 0, pbase = 0;
-    for (int s0 = 0; s0 < a.S; s0 += AT_THREADS) {
-        const int s = s0 + tid;
-        int it = 0, pt = 0, nsplit = 0;
-        if (s < a.S) {
-            const Request r = request_of(a, s, RB);
-            nsplit = max((int)(((int64_t)r.range + C - 1) / C), 1);
-            it = r.groups * nkv * nsplit;
-            pt = nsplit > 1 ? it : 0;
+        for (int d = 1; d < WAVE; d <<= 1) {
+            const int64_t o = __shfl_up(incl, d, WAVE);
+            if (l >= d) incl += o;
         }
-        const int ii = wave_incl_scan(it), pi = wave_incl_scan(pt);
-        __syncthreads();                    // the scratch's last readers are done
-        if (l == WAVE - 1) { sc32[0][w] = ii; sc32[1][w] = pi; }
+        total = __shfl(incl, WAVE - 1, WAVE);
+        my_base = incl - c;
+        if (blockIdx.x == 0 && w == 0 && l < a.S) a.base[l] = my_base;
+    } else {
+        total = 0;
+        for (int s0 = 0; s0 < a.S; s0 += AT_THREADS) {
+            const int s = s0 + tid;
+            int64_t c = 0;
+            if (s < a.S) {
+                const Request r = request_of(a, s, RB, STEP);
+                c = (int64_t)r.units * r.steps;
+            }
+            int64_t incl = c;
+#pragma unroll
+            for (int d = 1; d < WAVE; d <<= 1) {
+                const int64_t o = __shfl_up(incl, d, WAVE);
+                if (l >= d) incl += o;
+            }
+            __syncthreads();                // the scratch's last readers are done
+            if (l == WAVE - 1) sc64[w] = incl;
+            __syncthreads();
+            int64_t b = total;
+#pragma unroll
+            for (int i = 0; i < NW; i++) {
+                if (i < w) b += sc64[i];
+                total += sc64[i];
+            }
+            if (s < a.S) {
+                base[s] = b + incl - c;
+                if (blockIdx.x == 0) a.base[s] = b + incl - c;
+            }
+        }
+        if (tid == 0) base[a.S] = total;
         __syncthreads();
-        int ib = ibase, pb = pbase;
-#pragma unroll
-        for (int i = 0; i < NW; i++) {
-            if (i < w) { ib += sc32[0][i]; pb += sc32[1][i]; }
-            ibase += sc32[0][i];
-            pbase += sc32[1][i];
-        }
-        if (s < a.S) {
-            istart[s] = ib + ii - it;
-            pstart[s] = pb + pi - pt;
-            if (blockIdx.x == 0) a.meta[s] = make_int4(pb + pi - pt, nsplit, 0, 0);
-        }
     }
-    if (tid == 0) istart[a.S] = ibase;
-    __syncthreads();
-    const int items = istart[a.S];
+    const int64_t share = max((total + a.shares - 1) / a.shares, (int64_t)1);
+    if (blockIdx.x == 0 && tid == 0) a.share[0] = share;
+    const int64_t share_lo = blockIdx.x * share, share_hi = min(share_lo + share, total);
 
     const int r16 = l & 15, g4 = l >> 4;
     const float qscale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * LOG2E;
     const float capk = a.softcap * LOG2E;
     const int ps = a.kv.page_shift, pmask = (1 << ps) - 1;
 
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        int s = 0, hi = a.S;
-        while (hi - s > 1) {
-            const int mid = (s + hi) >> 1;
-            if (istart[mid] <= item) s = mid;
-            else hi = mid;
+    for (int64_t at = share_lo; at < share_hi;) {
+        int s;
+        Request rq;
+        int64_t s_base;
+        if (lanes) {
+            s = __popcll(__ballot(l < a.S && my_base <= at)) - 1;      // (empty requests share a base with their successor)
+            rq.row0 = __builtin_amdgcn_readlane(mine.row0, s);
+            rq.n = __builtin_amdgcn_readlane(mine.n, s);
+            rq.first = __builtin_amdgcn_readlane(mine.first, s);
+            rq.len = __builtin_amdgcn_readlane(mine.len, s);
+            rq.units = __builtin_amdgcn_readlane(mine.units, s);
+            rq.steps = __builtin_amdgcn_readlane(mine.steps, s);
+            s_base = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_base, s) |
+                     ((int64_t)__builtin_amdgcn_readlane((int)(my_base >> 32), s) << 32);
+        } else {
+            s = 0;
+            int hi = a.S;
+            while (hi - s > 1) {
+                const int mid = (s + hi) >> 1;
+                if (base[mid] <= at) s = mid;
+                else hi = mid;
+            }
+            s = __builtin_amdgcn_readfirstlane(s);
+            rq = request_of(a, s, RB, STEP);
+            s_base = base[s];
         }
-        const Request rq = request_of(a, s, RB);
-        const int nsplit = max((int)(((int64_t)rq.range + C - 1) / C), 1);
-        // item = (row group, kv head, split), split fastest
-        int x = item - istart[s];
-        const int split = x % nsplit;
-        x /= nsplit;
-        const int head = x % nkv, grp = x / nkv;
+        // the piece: steps [st0, st1) of unit (row group, head)
+        const int unit = (int)((at - s_base) / rq.steps);
+        const int st0 = (int)(at - s_base - (int64_t)unit * rq.steps);
+        const int st1 = (int)min((int64_t)rq.steps, st0 + (share_hi - at));
+        const int64_t piece_at = at;
+        at += st1 - st0;
+        const int grp = unit / nkv, head = unit - grp * nkv;
         const int row0 = grp * RB, nrows = min(RB, rq.n * G - row0);
         const int i0 = row0 / G, i1 = (row0 + nrows - 1) / G;
-        // positions [lo, hi) that some row of the item sees, and this split's part
+        // positions [see_lo, see_hi) that some row of the unit sees; the piece's
+        // steps are its share of them (units of a request have equally many
+        // steps, though the first rows of a long prompt see less)
         const int p_lo = rq.first + i0, p_hi = rq.first + i1;       // positions of its first and last row
         const int see_lo = a.window > 0 ? max(p_lo - a.window + 1, 0) : 0;
-        const int see_hi = min(p_hi + 1, rq.len);
+        const int see_hi = max(min(p_hi + 1, rq.len), 0);
         const int a0 = see_lo & ~(TILE - 1);
-        const int total = max(see_hi - a0, 0);
-        const int per = (int)(((int64_t)total + (int64_t)nsplit * TILE * NW - 1) / ((int64_t)nsplit * TILE * NW)) * (TILE * NW);
-        const int t_lo = (int)min((int64_t)a0 + (int64_t)split * per, (int64_t)see_hi);
-        const int t_hi = (int)min((int64_t)t_lo + per, (int64_t)see_hi);
+        const int real_steps = (max(see_hi - a0, 0) + STEP - 1) / STEP;
+        const int t_lo = min((int64_t)a0 + (int64_t)real_steps * st0 / rq.steps * STEP, (int64_t)see_hi);
+        const int t_hi = min((int64_t)a0 + (int64_t)real_steps * st1 / rq.steps * STEP, (int64_t)see_hi);
         // every row sees [full_lo, full_hi) whole
         const int full_lo = a.window > 0 ? max(p_hi - a.window + 1, 0) : 0;
         const int full_hi = min(p_lo + 1, rq.len);
 
-        // ---- the item's q rows: row r = query token i0.., head of the group
-        __syncthreads();                    // the last item's join area is read
-        if (tid == 0) strange = 0;
-        for (int c = tid; c < RB * (D / 8); c += AT_THREADS) {
-            const int rr = c / (D / 8), cc = c - rr * (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (rr < nrows) {
-                const int row = row0 + rr, i = row / G, g = row - i * G;
-                v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.row0 + i) * a.q_stride +
-                                                    (int64_t)(head * G + g) * D + cc * 8);
+        const table_ptr trow = (table_ptr)(uintptr_t)(a.table + (int64_t)s * a.W);
+        // pages of a tile's sub-tiles; -1: none (outside the cache, or past the piece)
+        struct Pages { int p[NSUB]; };
+        auto pages_of = [&](int t0) __attribute__((always_inline)) {
+            Pages e;
+#pragma unroll
+            for (int sb = 0; sb < NSUB; sb++) {
+                const int v = trow[min((t0 + 16 * sb) >> ps, a.W - 1)];
+                e.p[sb] = (v >= 0 && v < a.kv.num_pages && t0 < t_hi) ? v : -1;
             }
-            *reinterpret_cast<uint4*>(qs + rr * QP + cc * 8) = v;
-        }
-        __syncthreads();
-        // q fragments: bf16 keys: step k, lane group g4 holds chunk 4 k + g4; e4m3:
-        // chunk 4 (k / 2) + g4 of 16 elements, half k & 1
-        auto q_frag = [&](int mt, int k) __attribute__((always_inline)) {
-            const int d = F8 ? 16 * (4 * (k >> 1) + g4) + 8 * (k & 1) : 32 * k + 8 * g4;
-            return *reinterpret_cast<const bf16x8_t*>(qs + (mt * 16 + r16) * QP + d);
+            return e;
+        };
+        constexpr int ES = F8 ? 1 : 2, X = 16 / ES;          // element bytes, elements per key chunk
+        auto load_k = [&](TL& t, int t0, const Pages& pg) __attribute__((always_inline)) {
+#pragma unroll
+            for (int sb = 0; sb < NSUB; sb++) {
+                const int64_t ph = (int64_t)max(pg.p[sb], 0) * nkv + head;
+                const int off = (t0 + 16 * sb) & pmask;
+                const rsrc_t r = buffer_of((const char*)a.kv.k + (((ph * (D / X)) << ps) + off) * 16,
+                                           pg.p[sb] < 0 ? 0 : ((D / X) << ps) * 16 - off * 16);
+#pragma unroll
+                for (int c = 0; c < KV; c++) t.k[sb][c] = buf128(r, (((4 * c + g4) << ps) + r16) * 16);
+                if constexpr (F8)
+                    t.ks[sb] = __builtin_bit_cast(f32x4_t, buf128(buffer_of(a.kv.k_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
+            }
+        };
+        auto load_v = [&](TL& t, int t0, const Pages& pg) __attribute__((always_inline)) {
+#pragma unroll
+            for (int sb = 0; sb < NSUB; sb++) {
+                const int64_t ph = (int64_t)max(pg.p[sb], 0) * nkv + head;
+                const int off = (t0 + 16 * sb) & pmask;
+                const rsrc_t r = buffer_of((const char*)a.kv.v + ((ph << ps) + off) * D * ES, pg.p[sb] < 0 ? 0 : 16 * D * ES);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int h = 0; h < NH; h++) {
+                        const int at = (4 * g4 * D + r16 * E + j * D + h * 16 * E) * ES;
+                        uint32_t* v = t.v[4 * sb + j][h];
+                        if constexpr (EW == 4) {
+                            const u32x4_a q = buf128(r, at);
+#pragma unroll
+                            for (int i = 0; i < 4; i++) v[i % EW] = q[i];
+                        } else if constexpr (EW == 2) {
+                            const u32x2_a q = buf64(r, at);
+                            v[0] = q[0];
+                            v[1 % EW] = q[1];
+                        } else {
+                            v[0] = buf32(r, at);
+                        }
+                    }
+                if constexpr (F8)
+                    t.vs[sb] = __builtin_bit_cast(f32x4_t, buf128(buffer_of(a.kv.v_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
+            }
+        };
+
+        // ---- the unit's q rows (row r = query token i0.., head of the group), as
+        // the fragments of the first product: bf16 keys: step k, lane group g4
+        // holds chunk 4 k + g4; e4m3: chunk 4 (k / 2) + g4 of 16 elements, half k & 1
+        auto q_dim = [&](int k) __attribute__((always_inline)) {
+            return F8 ? 16 * (4 * (k >> 1) + g4) + 8 * (k & 1) : 32 * k + 8 * g4;
         };
         bf16x8_t qf[QREG ? MT : 1][QREG ? D / 32 : 1];
         if constexpr (QREG) {
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++)
+            for (int mt = 0; mt < MT; mt++) {
+                const int rr = min(mt * 16 + r16, nrows - 1);        // (rows past the unit's repeat its last, unused)
+                const int row = row0 + rr, i = row / G, g = row - i * G;
+                const uint16_t* src = a.q + (int64_t)(rq.row0 + i) * a.q_stride + (int64_t)(head * G + g) * D;
 #pragma unroll
-                for (int k = 0; k < D / 32; k++) qf[mt][k] = q_frag(mt, k);
+                for (int k = 0; k < D / 32; k++) qf[mt][k] = *reinterpret_cast<const bf16x8_t*>(src + q_dim(k));
+            }
         }
+        TL t;
+        const int t_first = t_lo + w * TILE;
+        Pages pg = pages_of(t_first), pg_next = pages_of(t_first + STEP);
+        load_k(t, t_first, pg);
+        load_v(t, t_first, pg);
+        __syncthreads();                    // the last piece's join area is read
+        if (tid == 0) strange = 0;
+        if constexpr (!QREG) {
+            for (int c = tid; c < RB * (D / 8); c += AT_THREADS) {
+                const int rr = c / (D / 8), cc = c - rr * (D / 8);
+                const int row = row0 + min(rr, nrows - 1), i = row / G, g = row - i * G;
+                *reinterpret_cast<uint4*>(qs + rr * QP + cc * 8) = *reinterpret_cast<const uint4*>(
+                    a.q + (int64_t)(rq.row0 + i) * a.q_stride + (int64_t)(head * G + g) * D + cc * 8);
+            }
+        }
+        __syncthreads();
+        auto q_frag = [&](int mt, int k) __attribute__((always_inline)) {
+            if constexpr (QREG) return qf[mt][k];
+            else return *reinterpret_cast<const bf16x8_t*>(qs + (mt * 16 + r16) * QP + q_dim(k));
+        };
         // this lane's row in each row tile: the positions it sees, [vlo, vhi]
         int vlo[MT], vhi[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            const int row = row0 + mt * 16 + r16, i = row / G;
-            const bool real = mt * 16 + r16 < nrows;
+            const int i = (row0 + mt * 16 + r16) / G;
             const int p = rq.first + i;
-            vhi[mt] = real ? min(p, rq.len - 1) : -1;
+            vhi[mt] = mt * 16 + r16 < nrows ? min(p, rq.len - 1) : -1;
             vlo[mt] = a.window > 0 ? max(p - a.window + 1, 0) : 0;
         }
 
@@ -266,65 +384,10 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                 for (int e = 0; e < E; e++) acc[mt][h][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        const int32_t* trow = a.table + (int64_t)s * a.W;
-        auto load = [&](TL& t, int t0, int (&page)[2]) __attribute__((always_inline)) {
+        // S^T of one row tile: [sub-tile][i], in units of log2
+        auto scores = [&](const TL& t, int mt, f32x4_t (&sc)[NSUB]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int sb = 0; sb < 2; sb++) {
-                const int pos = t0 + 16 * sb;
-                // sub-tiles past the table repeat its last page and are masked
-                const int e = trow[min(pos >> ps, a.W - 1)];
-                page[sb] = (e >= 0 && e < a.kv.num_pages) ? e : -1;
-                const int64_t ph = (int64_t)max(page[sb], 0) * nkv + head;
-                const int off = pos & pmask;
-                if constexpr (F8) {
-                    const uint8_t* kb = (const uint8_t*)a.kv.k + ((ph * (D / 16)) << (ps + 4)) + off * 16;
-#pragma unroll
-                    for (int c = 0; c < KV; c++)
-                        t.k[sb][c] = *reinterpret_cast<const u32x4_a*>(kb + (((4 * c + g4) << ps) + r16) * 16);
-                    const uint8_t* vb = (const uint8_t*)a.kv.v + ((ph << ps) + off) * D;
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-#pragma unroll
-                        for (int h = 0; h < NH; h++) {
-                            const uint8_t* src = vb + (4 * g4 + j) * D + h * 16 * E + r16 * E;
-                            if constexpr (EW == 2) {
-                                const u32x2_a q = *reinterpret_cast<const u32x2_a*>(src);
-                                t.v[4 * sb + j][h][0] = q[0];
-                                t.v[4 * sb + j][h][EW - 1] = q[1];
-                            } else {
-                                t.v[4 * sb + j][h][0] = *reinterpret_cast<const uint32_t*>(src);
-                            }
-                        }
-                    t.ks[sb] = *reinterpret_cast<const f32x4_t*>(a.kv.k_scale + (ph << ps) + off + 4 * g4);
-                    t.vs[sb] = *reinterpret_cast<const f32x4_t*>(a.kv.v_scale + (ph << ps) + off + 4 * g4);
-                } else {
-                    const uint16_t* kb = (const uint16_t*)a.kv.k + ((ph * (D / 8)) << (ps + 3)) + off * 8;
-#pragma unroll
-                    for (int c = 0; c < KV; c++)
-                        t.k[sb][c] = *reinterpret_cast<const u32x4_a*>(kb + (((4 * c + g4) << ps) + r16) * 8);
-                    const uint16_t* vb = (const uint16_t*)a.kv.v + ((ph << ps) + off) * D;
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-#pragma unroll
-                        for (int h = 0; h < NH; h++) {
-                            const uint16_t* src = vb + (4 * g4 + j) * D + h * 16 * E + r16 * E;
-                            if constexpr (EW == 4) {
-                                const u32x4_a q = *reinterpret_cast<const u32x4_a*>(src);
-#pragma unroll
-                                for (int i = 0; i < EW; i++) t.v[4 * sb + j][h][i] = q[i % 4];
-                            } else {
-                                const u32x2_a q = *reinterpret_cast<const u32x2_a*>(src);
-#pragma unroll
-                                for (int i = 0; i < EW; i++) t.v[4 * sb + j][h][i] = q[i % 2];
-                            }
-                        }
-                }
-            }
-        };
-        // S^T of one row tile: [sub-tile][i], in units of log2 (uncapped) or of the cap
-        auto scores = [&](const TL& t, int mt, f32x4_t (&sc)[2]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int sb = 0; sb < 2; sb++) {
+            for (int sb = 0; sb < NSUB; sb++) {
                 f32x4_t c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < D / 32; k++) {
@@ -337,7 +400,7 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                     } else {
                         kf = __builtin_bit_cast(bf16x8_t, t.k[sb][k]);
                     }
-                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, QREG ? qf[QREG ? mt : 0][QREG ? k : 0] : q_frag(mt, k), c, 0, 0, 0);
+                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q_frag(mt, k), c, 0, 0, 0);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -350,63 +413,64 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                 }
             }
         };
-        // O^T += V^T P^T, the P fragments given
-        auto values = [&](const TL& t, const u32x4_a (&p)[MT]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int h = 0; h < NH; h++) {
-                if constexpr (F8) {
-#pragma unroll
-                    for (int q = 0; q < EW; q++) {          // 4 elements of each position per word
-                        u32x4_a f[4];
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t x = t.v[2 * j][h][q], y = t.v[2 * j + 1][h][q];
-                            const uint32_t lo = __builtin_amdgcn_perm(y, x, 0x05010400);   // x0 y0 x1 y1
-                            const uint32_t hh = __builtin_amdgcn_perm(y, x, 0x07030602);   // x2 y2 x3 y3
-                            f[0][j] = fp8x2_bf16<false>(lo);
-                            f[1][j] = fp8x2_bf16<true>(lo);
-                            f[2][j] = fp8x2_bf16<false>(hh);
-                            f[3][j] = fp8x2_bf16<true>(hh);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-#pragma unroll
-                            for (int mt = 0; mt < MT; mt++)
-                                acc[mt][h][4 * q + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    __builtin_bit_cast(bf16x8_t, f[e]), __builtin_bit_cast(bf16x8_t, p[mt]),
-                                    acc[mt][h][4 * q + e], 0, 0, 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < EW; q++) {          // 2 elements of each position per word
-                        u32x4_a f[2];
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            const uint32_t x = t.v[2 * j][h][q], y = t.v[2 * j + 1][h][q];
-                            f[0][j] = __builtin_amdgcn_perm(y, x, 0x05040100);
-                            f[1][j] = __builtin_amdgcn_perm(y, x, 0x07060302);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; e++)
-#pragma unroll
-                            for (int mt = 0; mt < MT; mt++)
-                                acc[mt][h][2 * q + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    __builtin_bit_cast(bf16x8_t, f[e]), __builtin_bit_cast(bf16x8_t, p[mt]),
-                                    acc[mt][h][2 * q + e], 0, 0, 0);
-                    }
-                }
+        // O^T += V^T P^T over sub-tiles 2 pr and 2 pr + 1 (NSUB 1: the one there is)
+        constexpr int JP = NSUB == 1 ? 2 : 4;             // pairs of positions per product
+        auto mma = [&](const uint32_t (&f)[JP], const uint32_t (&p)[JP], f32x4_t c) __attribute__((always_inline)) {
+            if constexpr (NSUB == 1) {
+                return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_a, f),
+                                                                 __builtin_bit_cast(s16x4_a, p), c, 0, 0, 0);
+            } else {
+                return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f),
+                                                               __builtin_bit_cast(bf16x8_t, p), c, 0, 0, 0);
             }
         };
-        // running maximum and sum of one row tile; sc -> probabilities
-        auto soften = [&](f32x4_t (&sc)[2], int mt) __attribute__((always_inline)) {
-            float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                              fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+        auto values = [&](const TL& t, const uint32_t (&p)[MT][2 * NSUB]) __attribute__((always_inline)) {
+            constexpr int PER = F8 ? 4 : 2;               // elements per word
+#pragma unroll
+            for (int pr = 0; pr < 2 * NSUB / JP; pr++)
+#pragma unroll
+                for (int h = 0; h < NH; h++)
+#pragma unroll
+                    for (int q = 0; q < EW; q++) {
+                        uint32_t f[PER][JP];
+#pragma unroll
+                        for (int j = 0; j < JP; j++) {
+                            const uint32_t x = t.v[2 * (pr * JP + j)][h][q], y = t.v[2 * (pr * JP + j) + 1][h][q];
+                            if constexpr (F8) {
+                                const uint32_t lo = __builtin_amdgcn_perm(y, x, 0x05010400);   // x0 y0 x1 y1
+                                const uint32_t hh = __builtin_amdgcn_perm(y, x, 0x07030602);   // x2 y2 x3 y3
+                                f[0][j] = fp8x2_bf16<false>(lo);
+                                f[1][j] = fp8x2_bf16<true>(lo);
+                                f[PER - 2][j] = fp8x2_bf16<false>(hh);
+                                f[PER - 1][j] = fp8x2_bf16<true>(hh);
+                            } else {
+                                f[0][j] = __builtin_amdgcn_perm(y, x, 0x05040100);
+                                f[1][j] = __builtin_amdgcn_perm(y, x, 0x07060302);
+                            }
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; mt++) {
+                            uint32_t pp[JP];
+#pragma unroll
+                            for (int j = 0; j < JP; j++) pp[j] = p[mt][pr * JP + j];
+#pragma unroll
+                            for (int e = 0; e < PER; e++)
+                                acc[mt][h][PER * q + e] = mma(f[e], pp, acc[mt][h][PER * q + e]);
+                        }
+                    }
+        };
+        // running maximum of one row tile; sc -> probabilities
+        auto soften = [&](f32x4_t (&sc)[NSUB], int mt) __attribute__((always_inline)) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int sb = 0; sb < NSUB; sb++)
+                top = fmaxf(top, fmaxf(fmaxf(sc[sb][0], sc[sb][1]), fmaxf(sc[sb][2], sc[sb][3])));
             top = fmaxf(top, tr_partner<16>(top));
             top = fmaxf(top, tr_partner<32>(top));
             const float mn = fmaxf(m[mt], top);
-            const float base = mn == -__builtin_inff() ? 0.f : mn;       // a row that has seen nothing yet
+            const float base2 = mn == -__builtin_inff() ? 0.f : mn;      // a row that has seen nothing yet
             if (__any(mn > m[mt])) {
-                const float f = exp2f(m[mt] - base);
+                const float f = __builtin_amdgcn_exp2f(m[mt] - base2);
                 sum[mt] *= f;
 #pragma unroll
                 for (int h = 0; h < NH; h++)
@@ -415,48 +479,55 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                 m[mt] = mn;
             }
 #pragma unroll
-            for (int sb = 0; sb < 2; sb++)
+            for (int sb = 0; sb < NSUB; sb++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    sc[sb][i] = exp2f(sc[sb][i] - base);
-                    sum[mt] += sc[sb][i];
-                }
+                for (int i = 0; i < 4; i++) sc[sb][i] = __builtin_amdgcn_exp2f(sc[sb][i] - base2);
         };
-        auto pack_p = [&](const TL& t, const f32x4_t (&sc)[2]) __attribute__((always_inline)) -> u32x4_a {
-            u32x4_a p;
+        // the second product's operand, and the running sum of the weights as that
+        // product sees them: the sum of the rounded probabilities, so that their
+        // rounding (half a step of bf16) cancels where few positions dominate.
+        // e4m3 values: the weight is p v_scale, rounded; the sum takes it over v_scale.
+        auto pack_p = [&](const TL& t, const f32x4_t (&sc)[NSUB], int mt, uint32_t (&p)[2 * NSUB])
+                          __attribute__((always_inline)) {
 #pragma unroll
-            for (int sb = 0; sb < 2; sb++) {
+            for (int sb = 0; sb < NSUB; sb++) {
                 f32x4_t v = sc[sb];
                 if constexpr (F8)
 #pragma unroll
                     for (int i = 0; i < 4; i++) v[i] = v[i] == 0.f ? 0.f : v[i] * t.vs[sb][i];
                 p[2 * sb] = pk_bf16(v[0], v[1]);
                 p[2 * sb + 1] = pk_bf16(v[2], v[3]);
+                f32x4_t u = {bf16lo_to_f32(p[2 * sb]), bf16hi_to_f32(p[2 * sb]), bf16lo_to_f32(p[2 * sb + 1]),
+                             bf16hi_to_f32(p[2 * sb + 1])};
+                if constexpr (F8)
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        u[i] = u[i] == 0.f ? sc[sb][i] : u[i] * __builtin_amdgcn_rcpf(t.vs[sb][i]);
+                sum[mt] += (u[0] + u[1]) + (u[2] + u[3]);
             }
-            return p;
         };
+        // position of this lane's j-th value of the tile
+        auto pos_of = [&](int t0, int j) __attribute__((always_inline)) { return t0 + 16 * (j >> 2) + 4 * g4 + (j & 3); };
 
-        // every row sees all of the tile's positions
-        auto whole_tile = [&](int t0) {
-            if (t0 < full_lo || t0 + TILE > full_hi) return false;
-            const int e0 = trow[min(t0 >> ps, a.W - 1)], e1 = trow[min((t0 + 16) >> ps, a.W - 1)];
-            return e0 >= 0 && e0 < a.kv.num_pages && e1 >= 0 && e1 < a.kv.num_pages;
-        };
-        for (int t0 = t_lo + w * TILE; t0 < t_hi; t0 += NW * TILE) {
-            TL t;
-            int page[2];
-            load(t, t0, page);
-            const bool whole = t0 >= full_lo && t0 + TILE <= full_hi && page[0] >= 0 && page[1] >= 0;   // = whole_tile(t0)
+        // The tile's registers are refilled as they are used up: the next tile's
+        // keys load under this one's softmax and second product, its values under
+        // the next one's scores, and its pages are looked up a tile ahead.  (Past
+        // the last tile the loads return at once.)
+        for (int t0 = t_first; t0 < t_hi; t0 += STEP) {
+            bool pages = true;
+#pragma unroll
+            for (int sb = 0; sb < NSUB; sb++) pages = pages && pg.p[sb] >= 0;
+            const bool whole = pages && t0 >= full_lo && t0 + TILE <= full_hi;      // = whole_tile(t0)
             // tiles that some row sees in part: which of this lane's positions are
             // there at all; values that no row sees become 0
-            bool odd = false;               // an infinite or NaN value among those that are there
-            uint32_t there = 0xFFu;
+            uint32_t there = 0xFFFFFFFFu;
             if (!whole) {
+                bool odd = false;           // an infinite or NaN value among those that are there
                 there = 0;
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int pos = t0 + 16 * (j >> 2) + 4 * g4 + (j & 3);
-                    const bool in = page[j >> 2] >= 0 && pos >= see_lo && pos < see_hi;
+                for (int j = 0; j < 4 * NSUB; j++) {
+                    const int pos = pos_of(t0, j);
+                    const bool in = pg.p[j >> 2] >= 0 && pos >= see_lo && pos < see_hi;
                     there |= (in ? 1u : 0u) << j;
 #pragma unroll
                     for (int h = 0; h < NH; h++)
@@ -470,11 +541,11 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                 }
                 // 0 * inf is NaN: an infinite or NaN value must not meet the zero
                 // probability of a row that does not see it.  Such values become 0
-                // here and are added to the rows that see them when the item ends.
+                // here and are added to the rows that see them when the piece ends.
                 if (__any(odd)) {
                     strange = 1;
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
+                    for (int j = 0; j < 4 * NSUB; j++)
 #pragma unroll
                         for (int h = 0; h < NH; h++)
 #pragma unroll
@@ -493,24 +564,42 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
                             }
                 }
             }
-            u32x4_a p[MT];
+            f32x4_t sc[MT][NSUB];
+            if constexpr (!QREG) asm volatile("" ::: "memory");   // the q fragments are read again for every tile
 #pragma unroll
             for (int mt = 0; mt < MT; mt++) {
-                f32x4_t sc[2];
-                scores(t, mt, sc);
+                scores(t, mt, sc[mt]);
+                if constexpr (!QREG) __builtin_amdgcn_sched_barrier(0);   // one row tile's q fragments at a time
+            }
+            load_k(t, t0 + STEP, pg_next);
+            uint32_t p[MT][2 * NSUB];
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
                 if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const int pos = t0 + 16 * (j >> 2) + 4 * g4 + (j & 3);
-                        if (!((there >> j) & 1) || pos < vlo[mt] || pos > vhi[mt]) sc[j >> 2][j & 3] = -__builtin_inff();
+                    for (int j = 0; j < 4 * NSUB; j++) {
+                        const int pos = pos_of(t0, j);
+                        if (!((there >> j) & 1) || pos < vlo[mt] || pos > vhi[mt]) sc[mt][j >> 2][j & 3] = -__builtin_inff();
                     }
                 }
-                soften(sc, mt);
-                p[mt] = pack_p(t, sc);
+                soften(sc[mt], mt);
+                pack_p(t, sc[mt], mt, p[mt]);
             }
             values(t, p);
+            load_v(t, t0 + STEP, pg_next);
+            pg = pg_next;
+            pg_next = pages_of(t0 + 2 * STEP);
         }
 
+        // every row sees all of the tile's positions
+        auto whole_tile = [&](int t0) {
+            if (t0 < full_lo || t0 + TILE > full_hi) return false;
+            for (int pos = t0; pos < t0 + TILE; pos += 16) {
+                const int e = trow[min(pos >> ps, a.W - 1)];
+                if (e < 0 || e >= a.kv.num_pages) return false;
+            }
+            return true;
+        };
         // the infinite and NaN values left out above, of elements d .. d + 3 and the
         // positions that a row at position p sees (every probability is > 0)
         auto add_strange = [&](f32x4_t& o, int p, int d) {
@@ -533,22 +622,18 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
             }
         };
 
-        // ---- join the block's waves, one row tile at a time
-        const bool direct = nsplit == 1;
-        const int64_t pidx = direct ? 0 : (int64_t)pstart[s] + (item - istart[s]);
+        // ---- join the block's waves, one row tile at a time.  A unit that lies in
+        // this share alone is done; of others the piece that begins with the share
+        // is partial 2 b, one that begins inside it 2 b + 1.
+        const bool direct = st1 - st0 == rq.steps;
+        const int64_t pidx = 2 * (int64_t)blockIdx.x + (piece_at == share_lo ? 0 : 1);
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             float sm = sum[mt];
             sm += tr_partner<16>(sm);
             sm += tr_partner<32>(sm);
-            __syncthreads();                // q rows, or the row tile before, are read
+            if (mt > 0 || !QREG) __syncthreads();   // the row tile before, or the q rows, are read
             if (g4 == 0) jml[w * 16 + r16] = make_float2(m[mt], sm);
-            __syncthreads();
-            float M = jml[r16].x;
-#pragma unroll
-            for (int i = 1; i < NW; i++) M = fmaxf(M, jml[i * 16 + r16].x);
-            const float base = M == -__builtin_inff() ? 0.f : M;
-            const float f = exp2f(m[mt] - base);
             // lane: row r16; O^T rows 4 g4 + i of MFMA e are d = 16 E h + E (4 g4 + i) + e
 #pragma unroll
             for (int h = 0; h < NH; h++)
@@ -558,35 +643,36 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
 #pragma unroll
                     for (int e = 0; e < E; e += 4)
                         *reinterpret_cast<f32x4_t*>(dst + e) =
-                            f32x4_t{acc[mt][h][e][i] * f, acc[mt][h][e + 1][i] * f, acc[mt][h][e + 2][i] * f,
-                                    acc[mt][h][e + 3][i] * f};
+                            f32x4_t{acc[mt][h][e][i], acc[mt][h][e + 1][i], acc[mt][h][e + 2][i], acc[mt][h][e + 3][i]};
                 }
             __syncthreads();
             // 16 threads per row, D / 16 elements each, 4 at a time
             const int rr = tid >> 4, part = tid & 15, row = mt * 16 + rr;
             if (row < nrows) {
-                float Mr = jml[rr].x, L = 0.f;
+                float2 x[NW];
 #pragma unroll
-                for (int i = 1; i < NW; i++) Mr = fmaxf(Mr, jml[i * 16 + rr].x);
+                for (int i = 0; i < NW; i++) x[i] = jml[i * 16 + rr];
+                float Mr = x[0].x, L = 0.f, f[NW];
+#pragma unroll
+                for (int i = 1; i < NW; i++) Mr = fmaxf(Mr, x[i].x);
                 const float br = Mr == -__builtin_inff() ? 0.f : Mr;
 #pragma unroll
                 for (int i = 0; i < NW; i++) {
-                    const float2 x2 = jml[i * 16 + rr];
-                    L += x2.y * exp2f(x2.x - br);
+                    f[i] = __builtin_amdgcn_exp2f(x[i].x - br);
+                    L += x[i].y * f[i];
                 }
-                const float inv = L == 0.f ? 0.f : 1.0f / L;
+                const float inv = L == 0.f ? 0.f : 1.0f / L;         // (a row that sees nothing: 0)
                 const int grow = row0 + row, i = grow / G, g = grow - i * G;
                 uint16_t* dst = a.out + ((int64_t)(rq.row0 + i) * a.n_heads + head * G + g) * D;
                 float* pd = a.part + (pidx * RB + row) * D;
 #pragma unroll
                 for (int c = 0; c < D / 64; c++) {
                     const int d = c * 64 + part * 4;
-                    f32x4_t o = *reinterpret_cast<const f32x4_t*>(ja + rr * DP + d);
+                    f32x4_t o = *reinterpret_cast<const f32x4_t*>(ja + rr * DP + d) * f[0];
 #pragma unroll
-                    for (int i2 = 1; i2 < NW; i2++) o += *reinterpret_cast<const f32x4_t*>(ja + (i2 * 16 + rr) * DP + d);
+                    for (int i2 = 1; i2 < NW; i2++) o += *reinterpret_cast<const f32x4_t*>(ja + (i2 * 16 + rr) * DP + d) * f[i2];
                     if (strange) add_strange(o, rq.first + i, d);
                     if (direct) {
-                        // (a row that sees nothing: no sum, 0)
                         const u32x2_a q = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
                         *reinterpret_cast<u32x2_a*>(dst + d) = q;
                     } else {
@@ -599,61 +685,75 @@ __global__ __launch_bounds__(AT_THREADS) void k_paged_attn(const AttnArgs a) {
     }
 }
 
-// out = sum_c 2^{m_c - M} acc_c / sum_c 2^{m_c - M} sum_c over a request's splits,
-// in split order.  One wave per (row of the batch, head): D / 64 elements a lane.
-template <int D>
-__global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a, int rows_per_item) {
-    constexpr int EL = D / 64;
-    const int64_t id = (int64_t)blockIdx.x * NW + threadIdx.x / WAVE;
-    const int t = (int)(id / a.n_heads), hq = (int)(id - (int64_t)t * a.n_heads), l = lane_id();
-    if (t >= a.T) return;
+// out = sum_c 2^{m_c - M} acc_c / sum_c 2^{m_c - M} sum_c over the shares that a
+// unit lies in.  One block per (batch row, head, 64 elements): 16 threads of 4
+// elements, the shares dealt to 16 groups of them, joined through LDS in order.
+template <int D, int RB, int STEP>
+__global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
+    constexpr int NC = D / 64, NG = AT_THREADS / 16;
+    __shared__ float2 gml[NG];
+    __shared__ f32x4_t go[NG][16];
+    const int c = blockIdx.x % NC;
+    const int64_t id = blockIdx.x / NC;
+    const int t = (int)(id / a.n_heads), hq = (int)(id - (int64_t)t * a.n_heads);
     int s = 0, hi = a.S;
     while (hi - s > 1) {
         const int mid = (s + hi) >> 1;
         if (a.q_offsets[mid] <= t) s = mid;
         else hi = mid;
     }
-    const int4 me = a.meta[s];
-    const int nsplit = me.y;
-    const int b = max(a.q_offsets[s], 0);
-    if (nsplit <= 1 || t < b || t >= a.q_offsets[s + 1]) return;
+    const Request rq = request_of(a, s, RB, STEP);
+    const int64_t share = a.share[0];
+    if (t < rq.row0 || t >= rq.row0 + rq.n) return;
     const int nkv = a.kv.n_kv_heads, G = a.n_heads / nkv;
-    const int head = hq / G, row = (t - b) * G + (hq - head * G);
-    const int grp = row / rows_per_item, rr = row - grp * rows_per_item;
-    const int64_t p0 = (int64_t)me.x + ((int64_t)grp * nkv + head) * nsplit;
-    float M = -__builtin_inff();
-    for (int c = l; c < nsplit; c += WAVE) M = fmaxf(M, a.ml[(p0 + c) * rows_per_item + rr].x);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) M = fmaxf(M, wave_xor(M, d));
+    const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
+    const int grp = row / RB, rr = row - grp * RB;
+    const int64_t u0 = a.base[s] + ((int64_t)grp * nkv + head) * rq.steps;    // the unit's first step
+    const int64_t b0 = u0 / share;
+    const int np = (int)((u0 + rq.steps - 1) / share - b0) + 1;
+    if (np <= 1) return;
+    const int first_odd = u0 == b0 * share ? 0 : 1;
+    const int e = threadIdx.x & 15, gr = threadIdx.x >> 4;
+    float M = -__builtin_inff(), L = 0.f;
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int p = gr; p < np; p += NG) {
+        const int64_t at = (2 * (b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
+        const float2 x = a.ml[at];
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + at * D + c * 64 + e * 4);
+        const float mn = fmaxf(M, x.x), base = mn == -__builtin_inff() ? 0.f : mn;
+        const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(x.x - base);
+        L = L * f0 + x.y * f1;
+        o = o * f0 + v * f1;
+        M = mn;
+    }
+    if (e == 0) gml[gr] = make_float2(M, L);
+    go[gr][e] = o;
+    __syncthreads();
+    if (gr > 0) return;
+    for (int i = 0; i < NG; i++) M = fmaxf(M, gml[i].x);
     const float base = M == -__builtin_inff() ? 0.f : M;
-    float L = 0.f, o[EL];
-#pragma unroll
-    for (int e = 0; e < EL; e++) o[e] = 0.f;
-    for (int c = 0; c < nsplit; c++) {
-        const float2 x = a.ml[(p0 + c) * rows_per_item + rr];
-        const float f = exp2f(x.x - base);
+    L = 0.f;
+    o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NG; i++) {
+        const float2 x = gml[i];
+        const float f = __builtin_amdgcn_exp2f(x.x - base);
         L += x.y * f;
-        const float* src = a.part + ((p0 + c) * rows_per_item + rr) * D + l * EL;
-#pragma unroll
-        for (int e = 0; e < EL; e++) o[e] += src[e] * f;
+        o += go[i][e] * f;
     }
     const float inv = L == 0.f ? 0.f : 1.0f / L;
-    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + l * EL;
-#pragma unroll
-    for (int e = 0; e < EL; e++) dst[e] = f32_to_bf16_rne(o[e] * inv);
+    const u32x2_a q = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2_a*>(a.out + ((int64_t)t * a.n_heads + hq) * D + c * 64 + e * 4) = q;
 }
 
-// Rows per item: as many row tiles as a request has rows on average, so that
-// its cache is read once; more than 64 rows (16 at head_dim 256, where the
+// Row tiles per unit: as many as a request has rows on average, so that its
+// cache is read once; more than 64 rows (48 at head_dim 256, where the
 // accumulators take MT x 64 registers) go over it again.
 int row_tiles(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
     const int64_t rows = ((int64_t)T * (n_heads / n_kv_heads) + S - 1) / S;
-    const int most = head_dim == 256 ? 1 : 4;
+    const int most = head_dim == 256 ? 3 : 4;
     const int mt = (int)((rows + 15) / 16 < most ? (rows + 15) / 16 : most);
     return mt < 1 ? 1 : mt;
 }
-
-constexpr int TARGET_ITEMS = 512;           // two blocks on each of 256 CUs
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -661,29 +761,30 @@ struct AttnWs {
     size_t ml, part, total;
 };
 AttnWs attn_ws(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
-    const int rb = 16 * row_tiles(T, n_heads, n_kv_heads, head_dim, S);
-    // a request with two splits or more has ceil(range / C) <= 2 range / C of
-    // them per row group and head, and the ranges sum to at most target * C
-    const size_t parts = 2 * (size_t)TARGET_ITEMS;
+    const int mt = row_tiles(T, n_heads, n_kv_heads, head_dim, S), rb = 16 * mt;
+    const size_t parts = 2 * (size_t)shares_of(head_dim, mt);
     AttnWs w;
-    w.ml = up256((size_t)S * sizeof(int4));
+    w.ml = up256(((size_t)S + 1) * sizeof(int64_t));
     w.part = w.ml + up256(parts * rb * sizeof(float2));
     w.total = w.part + up256(parts * rb * head_dim * sizeof(float));
     return w;
 }
 
 template <int D, int F8, int MT>
-hipError_t launch_attn(const AttnArgs& a, hipStream_t st) {
+hipError_t launch_attn(AttnArgs a, hipStream_t st) {
+    using SH = Shape<D, F8, MT>;
     auto kern = k_paged_attn<D, F8, MT>;
-    const size_t head = ((size_t)(2 * a.S + 1) * 4 + 15) / 16 * 16;
-    const size_t join = sizeof(float) * NW * 16 * (D + 4) + sizeof(float2) * NW * 16, qrows = (size_t)16 * MT * (D + 8) * 2;
+    const size_t head = a.S <= WAVE ? 0 : ((size_t)(a.S + 1) * 8 + 15) / 16 * 16;
+    const size_t join = sizeof(float) * NW * 16 * (D + 4) + sizeof(float2) * NW * 16;
+    const size_t qrows = SH::QREG ? 0 : (size_t)16 * MT * (D + 8) * 2;
     const size_t lds = head + (join > qrows ? join : qrows);
     static LdsLimit lim;
     hipError_t e = lim.ensure((const void*)kern, 128 * 1024);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3(a.target), dim3(AT_THREADS), lds, st, a);
-    const int64_t waves = (int64_t)a.T * a.n_heads;
-    hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)((waves + NW - 1) / NW)), dim3(AT_THREADS), 0, st, a, 16 * MT);
+    a.shares = shares_of(D, MT);
+    hipLaunchKernelGGL(kern, dim3(a.shares), dim3(AT_THREADS), lds, st, a);
+    const int64_t blocks = (int64_t)a.T * a.n_heads * (D / 64);
+    hipLaunchKernelGGL((k_attn_join<D, 16 * MT, 16 * SH::NSUB * NW>), dim3((unsigned)blocks), dim3(AT_THREADS), 0, st, a);
     return hipGetLastError();
 }
 
@@ -691,12 +792,10 @@ template <int D, int F8>
 hipError_t launch_mt(const AttnArgs& a, int mt, hipStream_t st) {
     switch (mt) {
         case 1: return launch_attn<D, F8, 1>(a, st);
+        case 2: return launch_attn<D, F8, 2>(a, st);
+        case 3: return launch_attn<D, F8, 3>(a, st);
         default:
-            if constexpr (D < 256) {
-                if (mt == 2) return launch_attn<D, F8, 2>(a, st);
-                if (mt == 3) return launch_attn<D, F8, 3>(a, st);
-                return launch_attn<D, F8, 4>(a, st);
-            }
+            if constexpr (D < 256) return launch_attn<D, F8, 4>(a, st);
     }
     return hipErrorInvalidValue;
 }
@@ -713,8 +812,12 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     if (T == 0) return hipSuccess;
     const AttnWs L = attn_ws(T, n_heads, cache.n_kv_heads, cache.head_dim, S);
     char* wb = (char*)ws;
-    AttnArgs a{q,     q_stride, T,       n_heads, cache, table,        W,          q_offsets,           kv_len,
-               S,     scale,    softcap, window,  out,   TARGET_ITEMS, (int4*)wb, (float*)(wb + L.part), (float2*)(wb + L.ml)};
+    AttnArgs a{};
+    a.q = q; a.q_stride = q_stride; a.T = T; a.n_heads = n_heads; a.kv = cache;
+    a.table = table; a.W = W; a.q_offsets = q_offsets; a.kv_len = kv_len; a.S = S;
+    a.scale = scale; a.softcap = softcap; a.window = window; a.out = out;
+    a.share = (int64_t*)wb; a.base = (int64_t*)wb + 1;
+    a.ml = (float2*)(wb + L.ml); a.part = (float*)(wb + L.part);
     const int mt = row_tiles(T, n_heads, cache.n_kv_heads, cache.head_dim, S);
     const bool f8 = cache.k_scale != nullptr;
     switch (cache.head_dim) {

@@ -16,6 +16,8 @@
 #include "attn.h"
 #include "common.h"
 
+#include <algorithm>
+
 namespace {
 
 constexpr int ROPE_THREADS = 256;
@@ -27,19 +29,49 @@ MOE_DEV uint32_t pack2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// D: head_dim; F8: e4m3 cache; TB: rows per block
-template <int D, int F8, int TB>
+// D: head_dim; F8: e4m3 cache; TB: rows per block.  blockIdx.x: rows, blockIdx.y:
+// groups_per_block of the row's groups of HPW heads.  A wave takes every fourth
+// unit (row, group of heads) of the block, UN of them loaded together, the
+// next UN under the current ones; the first loads go out before the angles
+// are formed.
+template <int D, int F8, int TB, int UN>
 __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
     const uint16_t* __restrict__ qkv, int64_t stride, int T, int n_heads, KvView cache,
     const float* __restrict__ q_weight, const float* __restrict__ k_weight, float eps,
     const float* __restrict__ inv_freq, int R, int interleaved, float rope_scale, const int32_t* __restrict__ positions,
-    const int32_t* __restrict__ slots, uint16_t* __restrict__ q_out, int heads_per_block) {
+    const int32_t* __restrict__ slots, uint16_t* __restrict__ q_out, int groups_per_block) {
     constexpr int LPH = D / 8;             // lanes per head
     constexpr int HPW = WAVE / LPH;        // heads per wave
+    constexpr int NWV = ROPE_THREADS / WAVE;
     __shared__ float2 cs[TB * (D / 2)];    // (cos, sin) * rope_scale of the block's rows
+    __shared__ int row_slot[TB];
     const int t0 = blockIdx.x * TB;
     const int rows = min(TB, T - t0);
+    const int nk = cache.n_kv_heads, heads = n_heads + 2 * nk;
+    const int l = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int c8 = l % LPH, sub = l / LPH;
+    const int g_begin = blockIdx.y * groups_per_block;
+    const int groups = min((heads + HPW - 1) / HPW - g_begin, groups_per_block);
+    const int units = rows * groups;
+    auto load = [&](int u) __attribute__((always_inline)) -> uint4 {
+        u = min(u, units - 1);             // past the end: the last unit again, not used
+        const int r = u / groups, h = min((g_begin + u - r * groups) * HPW + sub, heads - 1);
+        return *reinterpret_cast<const uint4*>(qkv + (int64_t)(t0 + r) * stride + h * D + c8 * 8);
+    };
+    uint4 raw[UN];
+#pragma unroll
+    for (int i = 0; i < UN; i++) raw[i] = load(w + i * NWV);
+    float qw[8], kw[8];
+    const bool qn = q_weight != nullptr, kn = k_weight != nullptr;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const float4 a = qn ? *reinterpret_cast<const float4*>(q_weight + c8 * 8 + 4 * i) : make_float4(1, 1, 1, 1);
+        const float4 b = kn ? *reinterpret_cast<const float4*>(k_weight + c8 * 8 + 4 * i) : make_float4(1, 1, 1, 1);
+        qw[4 * i] = a.x; qw[4 * i + 1] = a.y; qw[4 * i + 2] = a.z; qw[4 * i + 3] = a.w;
+        kw[4 * i] = b.x; kw[4 * i + 1] = b.y; kw[4 * i + 2] = b.z; kw[4 * i + 3] = b.w;
+    }
     const int half = R / 2;
+    if ((int)threadIdx.x < rows) row_slot[threadIdx.x] = slots[t0 + threadIdx.x];
     for (int i = threadIdx.x; i < rows * half; i += ROPE_THREADS) {
         const int r = i / half, p = i - r * half;
         const double a = (double)positions[t0 + r] * (double)inv_freq[p];
@@ -50,43 +82,35 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
         cs[r * (D / 2) + p] = make_float2(c * rope_scale, s * rope_scale);
     }
     __syncthreads();
-    const int nk = cache.n_kv_heads, heads = n_heads + 2 * nk;
-    const int l = lane_id(), w = threadIdx.x / WAVE;
-    const int c8 = l % LPH, sub = l / LPH;
-    const int h_begin = blockIdx.y * heads_per_block, h_end = min(heads, h_begin + heads_per_block);
-    const int groups = (h_end - h_begin + HPW - 1) / HPW;
     const int page_mask = (1 << cache.page_shift) - 1;
     const int64_t cache_slots = (int64_t)cache.num_pages << cache.page_shift;
-    for (int u = w; u < rows * groups; u += ROPE_THREADS / WAVE) {
-        const int r = u / groups, h = h_begin + (u - r * groups) * HPW + sub;
-        const int t = t0 + r, slot = slots[t];
-        if (slot < 0 || slot >= cache_slots) continue;                     // a padding row (the same for the whole wave)
-        const bool have = h < h_end;
-        const uint4 raw = *reinterpret_cast<const uint4*>(qkv + (int64_t)t * stride + (have ? h : h_begin) * D + c8 * 8);
+    // the pair of chunk c in the half layout is chunk c +- R / 16 of the same head
+    const bool turned = c8 * 8 < R, second = c8 >= R / 16;
+    const int pair_lane = sub * LPH + (turned ? (second ? c8 - R / 16 : c8 + R / 16) : c8);
+    const int pair_chunk = second ? c8 - R / 16 : c8;
+    auto unit = [&](int u, uint4 rw) __attribute__((always_inline)) {
+        const int r = u / groups, h = (g_begin + u - r * groups) * HPW + sub;
+        const int t = t0 + r, slot = __builtin_amdgcn_readfirstlane(row_slot[r]);
+        if (slot < 0 || slot >= cache_slots) return;                       // a padding row (the same for the whole wave)
         float x[8];
-        const uint32_t u4[4] = {raw.x, raw.y, raw.z, raw.w};
+        const uint32_t u4[4] = {rw.x, rw.y, rw.z, rw.w};
 #pragma unroll
         for (int i = 0; i < 4; i++) { x[2 * i] = bf16lo_to_f32(u4[i]); x[2 * i + 1] = bf16hi_to_f32(u4[i]); }
         const bool is_q = h < n_heads, is_v = h >= n_heads + nk;
-        const float* wt = is_q ? q_weight : k_weight;
-        if (q_weight || k_weight) {
+        if (qn || kn) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
             for (int d = 1; d < LPH; d <<= 1) ss += wave_xor(ss, d);
-            if (wt && !is_v) {
+            if (!is_v && (is_q ? qn : kn)) {
                 const float inv = 1.0f / sqrtf(ss * (1.0f / D) + eps);
-                const float4 wa = *reinterpret_cast<const float4*>(wt + c8 * 8);
-                const float4 wb = *reinterpret_cast<const float4*>(wt + c8 * 8 + 4);
-                const float ww[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-                for (int i = 0; i < 8; i++) x[i] = x[i] * inv * ww[i];
+                for (int i = 0; i < 8; i++) x[i] = x[i] * inv * (is_q ? qw[i] : kw[i]);
             }
         }
-        const bool rot = !is_v && c8 * 8 < R;
         if (interleaved) {
-            if (rot) {
+            if (!is_v && turned) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float2 a = cs[r * (D / 2) + c8 * 4 + i];
@@ -96,70 +120,87 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
                 }
             }
         } else if (R > 0) {
-            // the pair of chunk c is chunk c +- R / 16 of the same head
-            const int pc = c8 < R / 16 ? c8 + R / 16 : c8 - R / 16;
-            const int src = sub * LPH + (rot ? pc : c8);
-            const bool second = c8 >= R / 16;
             float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = __shfl(x[i], src, WAVE);
-            if (rot) {
-                const int p0 = r * (D / 2) + (second ? c8 - R / 16 : c8) * 8;
+            for (int i = 0; i < 8; i++) y[i] = __shfl(x[i], pair_lane, WAVE);
+            if (!is_v && turned) {
+                const float2* ang = cs + r * (D / 2) + pair_chunk * 8;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float2 a = cs[p0 + i];
-                    x[i] = second ? x[i] * a.x + y[i] * a.y : x[i] * a.x - y[i] * a.y;
-                }
+                for (int i = 0; i < 8; i++) x[i] = x[i] * ang[i].x + (second ? y[i] : -y[i]) * ang[i].y;
             }
         }
-        float amax = 0.f;
+        if (is_q) {
+            uint4 o;
+            o.x = pack2(x[0], x[1]); o.y = pack2(x[2], x[3]); o.z = pack2(x[4], x[5]); o.w = pack2(x[6], x[7]);
+            *reinterpret_cast<uint4*>(q_out + ((int64_t)t * n_heads + h) * D + c8 * 8) = o;
+        }
+        if ((g_begin + u - r * groups) * HPW + HPW - 1 < n_heads) return;  // all of the wave's heads are q heads
+        const int kh = is_v ? h - n_heads - nk : h - n_heads;
+        const int64_t ph = (int64_t)(slot >> cache.page_shift) * nk + kh;  // (page, head)
+        const int off = slot & page_mask;
+        const bool kv = !is_q && h < heads;
         if constexpr (F8) {
-            bool nan = false;
+            float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                amax = fmaxf(amax, fabsf(x[i]));
-                nan |= x[i] != x[i];
-            }
-            if (nan) amax = __builtin_nanf("");
+            for (int i = 0; i < 8; i++) amax = (x[i] != x[i] || amax != amax) ? __builtin_nanf("") : fmaxf(amax, fabsf(x[i]));
 #pragma unroll
             for (int d = 1; d < LPH; d <<= 1) {
                 const float o = wave_xor(amax, d);
                 amax = (o != o || amax != amax) ? __builtin_nanf("") : fmaxf(amax, o);
             }
-        }
-        if (!have) continue;
-        if (is_q) {
-            uint4 o;
-            o.x = pack2(x[0], x[1]); o.y = pack2(x[2], x[3]); o.z = pack2(x[4], x[5]); o.w = pack2(x[6], x[7]);
-            *reinterpret_cast<uint4*>(q_out + ((int64_t)t * n_heads + h) * D + c8 * 8) = o;
-            continue;
-        }
-        const int kh = is_v ? h - n_heads - nk : h - n_heads;
-        const int64_t ph = (int64_t)(slot >> cache.page_shift) * nk + kh;    // (page, head)
-        const int off = slot & page_mask;
-        if constexpr (F8) {
-            // a head of zeros (or so small that its scale would be subnormal) is stored as zeros of scale 0
-            float sc = amax / 448.0f;
-            if (sc < 1.17549435e-38f) sc = 0.f;
-            const float dv = sc == 0.f ? 1.0f : sc;
+            // element = x / (amax / 448) as (7/8 x) / (amax / 512): both operands are
+            // exact for a bf16 x, so only the quotient rounds and a value that lies
+            // halfway between two e4m3 goes to the even one.  A head of zeros (or so
+            // small that amax / 512 would be subnormal) is stored as zeros of scale 0.
+            float sc = amax / 448.0f, dv = amax * (1.0f / 512);
+            if (sc < 2.36e-38f) { sc = 0.f; dv = 1.f; }
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) y[i] = 0.875f * x[i] / dv;
             uint32_t a = 0, b = 0;
-            a = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] / dv, x[1] / dv, a, false);
-            a = __builtin_amdgcn_cvt_pk_fp8_f32(x[2] / dv, x[3] / dv, a, true);
-            b = __builtin_amdgcn_cvt_pk_fp8_f32(x[4] / dv, x[5] / dv, b, false);
-            b = __builtin_amdgcn_cvt_pk_fp8_f32(x[6] / dv, x[7] / dv, b, true);
+            a = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], a, false);
+            a = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], a, true);
+            b = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], b, false);
+            b = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], b, true);
             // k: 16-element chunks, page_size of them side by side; v: rows
             const int64_t at = is_v ? (((ph << cache.page_shift) + off) * D + c8 * 8)
                                     : ((((ph * (D / 16) + (c8 >> 1)) << cache.page_shift) + off) * 16 + (c8 & 1) * 8);
-            *reinterpret_cast<u32x2_r*>((uint8_t*)(is_v ? cache.v : cache.k) + at) = u32x2_r{a, b};
-            if (c8 == 0) (is_v ? cache.v_scale : cache.k_scale)[(ph << cache.page_shift) + off] = sc;
+            if (kv) {
+                *reinterpret_cast<u32x2_r*>((uint8_t*)(is_v ? cache.v : cache.k) + at) = u32x2_r{a, b};
+                if (c8 == 0) (is_v ? cache.v_scale : cache.k_scale)[(ph << cache.page_shift) + off] = sc;
+            }
         } else {
             uint4 o;
             o.x = pack2(x[0], x[1]); o.y = pack2(x[2], x[3]); o.z = pack2(x[4], x[5]); o.w = pack2(x[6], x[7]);
             const int64_t at = is_v ? (((ph << cache.page_shift) + off) * D + c8 * 8)
                                     : ((((ph * (D / 8) + c8) << cache.page_shift) + off) * 8);
-            *reinterpret_cast<uint4*>((uint16_t*)(is_v ? cache.v : cache.k) + at) = o;
+            if (kv) *reinterpret_cast<uint4*>((uint16_t*)(is_v ? cache.v : cache.k) + at) = o;
         }
+    };
+    for (int u0 = w; u0 < units; u0 += UN * NWV) {
+        uint4 next[UN];
+        if (u0 + UN * NWV < units) {
+#pragma unroll
+            for (int i = 0; i < UN; i++) next[i] = load(u0 + (UN + i) * NWV);
+        }
+#pragma unroll
+        for (int i = 0; i < UN; i++)
+            if (u0 + i * NWV < units) unit(u0 + i * NWV, raw[i]);
+#pragma unroll
+        for (int i = 0; i < UN; i++) raw[i] = next[i];
     }
+}
+
+template <int D, int F8, int TB, int UN>
+void launch_t(int groups_per_block, const uint16_t* qkv, int64_t stride, int T, int n_heads, const KvView& cache,
+              const float* qw, const float* kw, float eps, const float* inv_freq, int R, int inter, float rope_scale,
+              const int32_t* positions, const int32_t* slots, uint16_t* q_out, hipStream_t st) {
+    constexpr int HPW = WAVE / (D / 8);
+    const int groups = (n_heads + 2 * cache.n_kv_heads + HPW - 1) / HPW;
+    hipLaunchKernelGGL((k_qk_norm_rope<D, F8, TB, UN>),
+                       dim3((T + TB - 1) / TB, (groups + groups_per_block - 1) / groups_per_block), dim3(ROPE_THREADS), 0,
+                       st, qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions, slots,
+                       q_out, groups_per_block);
 }
 
 template <int D, int F8>
@@ -167,19 +208,17 @@ hipError_t launch_d(const uint16_t* qkv, int64_t stride, int T, int n_heads, con
                     const float* kw, float eps, const float* inv_freq, int R, int inter, float rope_scale,
                     const int32_t* positions, const int32_t* slots, uint16_t* q_out, hipStream_t st) {
     constexpr int HPW = WAVE / (D / 8);
-    const int heads = n_heads + 2 * cache.n_kv_heads;
-    if (T <= 256) {
-        // few rows: one row's heads over several blocks, one wave pass each
-        const int hpb = HPW * (ROPE_THREADS / WAVE);
-        hipLaunchKernelGGL((k_qk_norm_rope<D, F8, 1>), dim3(T, (heads + hpb - 1) / hpb), dim3(ROPE_THREADS), 0, st, qkv,
-                           stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions, slots,
-                           q_out, hpb);
-    } else {
-        constexpr int TB = 16;
-        hipLaunchKernelGGL((k_qk_norm_rope<D, F8, TB>), dim3((T + TB - 1) / TB, 1), dim3(ROPE_THREADS), 0, st, qkv,
-                           stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions, slots,
-                           q_out, heads);
-    }
+    const int groups = (n_heads + 2 * cache.n_kv_heads + HPW - 1) / HPW;
+    // 8 rows per block (their keys' 16-byte chunks fill whole lines), the heads
+    // split until there are about 1024 blocks; few rows: one row and one group
+    // of heads per wave
+    if ((int64_t)T * groups <= 4096)
+        launch_t<D, F8, 1, 1>(4, qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions,
+                              slots, q_out, st);
+    else
+        launch_t<D, F8, 8, 4>((int)std::max<int64_t>(std::min<int64_t>((int64_t)groups * ((T + 7) / 8) / 1024, groups), 2),
+                              qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions,
+                              slots, q_out, st);
     return hipGetLastError();
 }
 

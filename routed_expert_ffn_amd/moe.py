@@ -526,17 +526,28 @@ def layer(x, w_router, wg, wu, wd, K: int, bias=None, sg=None, su=None, sd=None,
 _FP8 = torch.float8_e4m3fn
 
 
-def _elsewhere(dev, stream) -> bool:
+def _elsewhere(dev: int, stream) -> bool:
     """Whether a call has to switch to its tensors' device or to the given stream first (outputs and
     workspaces it allocates then belong to that stream)."""
-    return stream is not None or dev.index != torch.cuda.current_device()
+    return stream is not None or (dev >= 0 and dev != torch.cuda.current_device())
 
 
-def _on(dev, t, name, dtype=None, shape=None):
+def _current(dev: int) -> int:
+    """The current stream of a device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(dev: int, t, name, dtype=None, shape=None):
+    """t's address, after the checks (one pass over them where all hold)."""
+    if t.get_device() == dev and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape) \
+            and t.is_contiguous() and dev >= 0:
+        return t.data_ptr()
     _need(t, name, dtype, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, expected device {dev}")
+
+
+def _opt(dev: int, t, name, dtype, shape):
+    return None if t is None else _on(dev, t, name, dtype, shape)
 
 
 def _rows(t, name, dtype):
@@ -563,7 +574,7 @@ class KVCache:
         if k.dim() != 5 or k.shape[4] != 16 // k.element_size():
             raise ValueError(f"k has shape {tuple(k.shape)}, expected [pages][kv heads][head_dim / X][page size][X]")
         pages, heads, chunks, page, x = k.shape
-        dev = k.device
+        dev = k.get_device()
         _on(dev, v, "v", k.dtype, (pages, heads, page, chunks * x))
         if (k.dtype == _FP8) != (k_scale is not None) or (k.dtype == _FP8) != (v_scale is not None):
             raise ValueError("k_scale and v_scale belong to a float8 cache")
@@ -592,9 +603,15 @@ class KVCache:
 
 
 class KVPlan:
-    """The outputs of kv_plan: q_offsets [S+1], kv_len [S], positions [T], slots [T], counts [2], int32."""
+    """The outputs of kv_plan for S requests and T rows: q_offsets [S+1], kv_len [S], positions [T], slots [T],
+    counts [2], int32."""
 
     def __init__(self, q_offsets, kv_len, positions, slots, counts):
+        dev, i32 = q_offsets.get_device(), torch.int32
+        self.S, self.T, self.device = kv_len.numel(), slots.numel(), dev
+        self.ptrs = (_on(dev, q_offsets, "q_offsets", i32, (self.S + 1,)), _on(dev, kv_len, "kv_len", i32, (self.S,)),
+                     _on(dev, positions, "positions", i32, (self.T,)), _on(dev, slots, "slots", i32, (self.T,)),
+                     _on(dev, counts, "counts", i32, (2,)))
         self.q_offsets, self.kv_len, self.positions, self.slots, self.counts = q_offsets, kv_len, positions, slots, counts
 
     @classmethod
@@ -605,25 +622,17 @@ class KVPlan:
 def kv_plan(cached_len, new_len, free_pages, page_table, page_size: int, T: int, out=None, stream=None) -> KVPlan:
     """One step's page tables and slots from the requests' lengths (moe_kv_plan): new pages are taken from
     free_pages into page_table [S][W] (in place); out: optional KVPlan to fill."""
-    dev = cached_len.device
+    dev, i32 = cached_len.get_device(), torch.int32
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return kv_plan(cached_len, new_len, free_pages, page_table, page_size, T, out=out)
-    i32 = torch.int32
-    _need(cached_len, "cached_len", i32)
     S, W = page_table.shape
-    _on(dev, cached_len, "cached_len", i32, (S,))
-    _on(dev, new_len, "new_len", i32, (S,))
-    _on(dev, free_pages, "free_pages", i32)
-    _on(dev, page_table, "page_table", i32)
-    p = out if out is not None else KVPlan.allocate(S, T, dev)
-    if out is not None:
-        for n, t, m in (("q_offsets", p.q_offsets, S + 1), ("kv_len", p.kv_len, S), ("positions", p.positions, T),
-                        ("slots", p.slots, T), ("counts", p.counts, 2)):
-            _on(dev, t, n, i32, (m,))
-    _chk(load().moe_kv_plan(_ptr(cached_len), _ptr(new_len), S, _ptr(free_pages), free_pages.numel(), page_size, T,
-                            _ptr(page_table), W, _ptr(p.q_offsets), _ptr(p.kv_len), _ptr(p.positions), _ptr(p.slots),
-                            _ptr(p.counts), _stream()), "moe_kv_plan")
+    a, b = _on(dev, cached_len, "cached_len", i32, (S,)), _on(dev, new_len, "new_len", i32, (S,))
+    f, t = _on(dev, free_pages, "free_pages", i32), _on(dev, page_table, "page_table", i32)
+    p = out if out is not None else KVPlan.allocate(S, T, cached_len.device)
+    if (p.S, p.T, p.device) != (S, T, dev):
+        raise ValueError(f"out holds {p.S} requests and {p.T} rows on device {p.device}, expected {S}, {T} on {dev}")
+    _chk(load().moe_kv_plan(a, b, S, f, free_pages.numel(), page_size, T, t, W, *p.ptrs, _current(dev)), "moe_kv_plan")
     return p
 
 
@@ -632,11 +641,12 @@ def qk_norm_rope(qkv, cache: KVCache, positions, slots, q_weight=None, k_weight=
     """Head norms, rotation and cache write of the fused projection's rows qkv [T][(n_heads + 2 n_kv_heads) *
     head_dim] (moe_qk_norm_rope).  The rotated part of a head is twice inv_freq's length.  Returns q
     [T][n_heads][head_dim] (out: optional tensor to fill)."""
-    dev = qkv.device
+    dev = qkv.get_device()
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return qk_norm_rope(qkv, cache, positions, slots, q_weight, k_weight, eps, inv_freq, interleaved,
                                 rope_scale, out)
+    f32, i32 = torch.float32, torch.int32
     stride = _rows(qkv, "qkv", torch.bfloat16)
     T, n = qkv.shape
     D = cache.head_dim
@@ -644,20 +654,14 @@ def qk_norm_rope(qkv, cache: KVCache, positions, slots, q_weight=None, k_weight=
     if n % D or Hq <= 0:
         raise ValueError(f"qkv rows of {n} elements are not (n_heads + 2 * {cache.n_kv_heads}) heads of {D}")
     if cache.device != dev:
-        raise ValueError(f"the cache is on {cache.device}, expected {dev}")
-    _on(dev, positions, "positions", torch.int32, (T,))
-    _on(dev, slots, "slots", torch.int32, (T,))
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _on(dev, t, name, torch.float32, (D,))
-    R = 0
-    if inv_freq is not None:
-        R = 2 * _on(dev, inv_freq, "inv_freq", torch.float32).numel()
-    q = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    _on(dev, q, "out", torch.bfloat16, (T, Hq, D))
-    _chk(load().moe_qk_norm_rope(_ptr(qkv), BF16, stride, T, Hq, cache.ref, _ptr(q_weight), _ptr(k_weight), eps,
-                                 _ptr(inv_freq), R, 1 if interleaved else 0, rope_scale, _ptr(positions), _ptr(slots),
-                                 _ptr(q), _stream()), "moe_qk_norm_rope")
+        raise ValueError(f"the cache is on device {cache.device}, expected {dev}")
+    q = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=qkv.device)
+    _chk(load().moe_qk_norm_rope(qkv.data_ptr(), BF16, stride, T, Hq, cache.ref,
+                                 _opt(dev, q_weight, "q_weight", f32, (D,)), _opt(dev, k_weight, "k_weight", f32, (D,)),
+                                 eps, _opt(dev, inv_freq, "inv_freq", f32, None),
+                                 0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, rope_scale,
+                                 _on(dev, positions, "positions", i32, (T,)), _on(dev, slots, "slots", i32, (T,)),
+                                 _on(dev, q, "out", torch.bfloat16, (T, Hq, D)), _current(dev)), "moe_qk_norm_rope")
     return q
 
 
@@ -669,32 +673,34 @@ def paged_attention(q, cache: KVCache, page_table, q_offsets, kv_len, scale=None
                     workspace=None, stream=None):
     """Attention of the rows q [T][n_heads][head_dim] over their requests' cached positions (moe_paged_attn);
     scale defaults to head_dim ** -0.5.  Rows of q may lie apart.  Returns out [T][n_heads][head_dim]."""
-    dev = q.device
+    dev = q.get_device()
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return paged_attention(q, cache, page_table, q_offsets, kv_len, scale, softcap, window, out, workspace)
+    i32 = torch.int32
     if q.dim() != 3:
         raise ValueError("q must be [T][n_heads][head_dim]")
     T, Hq, D = q.shape
+    stride = Hq * D
+    if not q.is_contiguous():
+        if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D):
+            raise ValueError("a row of q must be contiguous")
+        stride = q.stride(0)
     if not q.is_cuda:
         raise ValueError("q must be a device tensor")
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise TypeError(f"q must be torch.bfloat16, not {q.dtype}")
-    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != D):
-        raise ValueError("a row of q must be contiguous")
     if cache.device != dev or cache.head_dim != D:
-        raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}, q has {D} on {dev}")
+        raise ValueError(f"the cache has heads of {cache.head_dim} on device {cache.device}, q has {D} on {dev}")
     S, W = page_table.shape
-    _on(dev, page_table, "page_table", torch.int32)
-    _on(dev, q_offsets, "q_offsets", torch.int32, (S + 1,))
-    _on(dev, kv_len, "kv_len", torch.int32, (S,))
-    o = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    _on(dev, o, "out", torch.bfloat16, (T, Hq, D))
+    o = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     nb = paged_attention_workspace_size(T, Hq, cache.n_kv_heads, D, S)
-    ws = _workspace(nb, dev, workspace)
-    _chk(load().moe_paged_attn(_ptr(q), BF16, q.stride(0) if T > 1 else Hq * D, T, Hq, cache.ref, _ptr(page_table), W,
-                               _ptr(q_offsets), _ptr(kv_len), S, D ** -0.5 if scale is None else scale, softcap,
-                               window, _ptr(o), _ptr(ws), max(nb, 1), _stream()), "moe_paged_attn")
+    ws = _workspace(nb, q.device, workspace)
+    _chk(load().moe_paged_attn(q.data_ptr(), BF16, stride, T, Hq, cache.ref, _on(dev, page_table, "page_table", i32), W,
+                               _on(dev, q_offsets, "q_offsets", i32, (S + 1,)), _on(dev, kv_len, "kv_len", i32, (S,)), S,
+                               D ** -0.5 if scale is None else scale, softcap, window,
+                               _on(dev, o, "out", torch.bfloat16, (T, Hq, D)), _on(dev, ws, "workspace"), nb,
+                               _current(dev)), "moe_paged_attn")
     return o
 
 
@@ -709,26 +715,22 @@ def linear(x, w, bias=None, act=None, residual=None, out_dtype=None, out=None, w
     """act(x w^T + bias) + residual in one rounding (moe_linear): x [T][K] (rows may lie apart) and w [N][K]
     bfloat16, bias [N] fp32, act None, "silu", "gelu", "gelu_tanh" or "relu", residual [T][N] in the output's
     dtype (bfloat16 or float32; out may be the residual)."""
-    dev = x.device
+    dev = x.get_device()
     if _elsewhere(dev, stream):
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return linear(x, w, bias, act, residual, out_dtype, out, workspace)
     stride = _rows(x, "x", torch.bfloat16)
     T, K = x.shape
     N = w.shape[0]
-    _on(dev, w, "w", torch.bfloat16, (N, K))
     if act not in _ACT:
         raise ValueError(f"unknown activation {act!r}")
-    if bias is not None:
-        _on(dev, bias, "bias", torch.float32, (N,))
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
-    if residual is not None:
-        _on(dev, residual, "residual", out_dtype, (T, N))
-    o = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=dev)
-    _on(dev, o, "out", out_dtype, (T, N))
+    o = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=x.device)
     nb = linear_workspace_size(T, N, K)
-    ws = _workspace(nb, dev, workspace) if nb else None
-    _chk(load().moe_linear(_ptr(x), BF16, stride, _ptr(w), BF16, _ptr(bias), _ACT[act], _ptr(residual), T, N, K,
-                           _ptr(o), _act_dtype(o), _ptr(ws), nb, _stream()), "moe_linear")
+    ws = _on(dev, _workspace(nb, x.device, workspace), "workspace") if nb else None
+    _chk(load().moe_linear(x.data_ptr(), BF16, stride, _on(dev, w, "w", torch.bfloat16, (N, K)), BF16,
+                           _opt(dev, bias, "bias", torch.float32, (N,)), _ACT[act],
+                           _opt(dev, residual, "residual", out_dtype, (T, N)), T, N, K,
+                           _on(dev, o, "out", out_dtype, (T, N)), _act_dtype(o), ws, nb, _current(dev)), "moe_linear")
     return o
