@@ -96,7 +96,10 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
     if (!page_table || !q_offsets || !kv_len || (T > 0 && (!q || !out))) return MOE_ERR_INVALID_ARG;
     if (q_stride < (int64_t)n_heads * kv.head_dim || (int64_t)T * n_heads > INT32_MAX) return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_BF16 || S_ > MAX_REQUESTS || n_heads % kv.n_kv_heads != 0 ||
-        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
+        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)n_heads * kv.head_dim > 64 * 65535 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
+        return MOE_ERR_UNSUPPORTED;
+    // the steps of all units (16 rows of a key-value head, 64 positions at least) are counted in int32
+    if ((((int64_t)T * n_heads + 15) / 16 + (int64_t)S_ * kv.n_kv_heads) * (((int64_t)W << kv.page_shift) / 64 + 1) > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !aligned4(page_table) || !aligned4(q_offsets) || !aligned4(kv_len))
         return MOE_ERR_UNSUPPORTED;

@@ -23,9 +23,10 @@
 //
 // The work, for a balanced load whatever the lengths: a unit is (request, row
 // group, key-value head), its length in steps of 32 NW positions; all units'
-// steps in a row are cut into equal shares, one per block.  A block walks the
-// pieces of units in its share; a unit that lies in several shares leaves a
-// partial result in each, which k_attn_join adds up in the order of the shares.
+// steps in a row, with a constant for each unit, are cut into equal shares, one
+// per block.  A block walks the pieces of units in its share; a unit that lies in
+// several shares leaves a partial result in each, which k_attn_join adds up in
+// the order of the shares.
 //
 // Bound by HBM at few rows: each cached byte is used for 16 MT rows at a time.
 #include "attn.h"
@@ -44,6 +45,7 @@ typedef uint32_t u32x4_a __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_a __attribute__((ext_vector_type(2)));
 typedef short s16x4_a __attribute__((ext_vector_type(4)));
 
+MOE_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 MOE_DEV uint32_t pk_bf16(float lo, float hi) {
     const bf16x2_a v = {(__bf16)lo, (__bf16)hi};
     return __builtin_bit_cast(uint32_t, v);
@@ -53,11 +55,10 @@ template <bool HI>
 MOE_DEV uint32_t fp8x2_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
-MOE_DEV int64_t wave_sum64(int64_t v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, WAVE);
-    return v;
-}
+
+// What a piece costs besides its steps (its q rows, first loads and join), in
+// steps: short requests would otherwise pile up in few shares.
+constexpr int PIECE_COST = 2;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -72,9 +73,11 @@ struct AttnArgs {
     float scale, softcap;
     int window;
     uint16_t* out;
+    int G;                                  // query heads per key-value head
+    int G16;                                // ceil(2^16 / G): x / G = x G16 >> 16 for x < 1024
     int shares;                             // blocks of the attention launch
-    int64_t* share;                         // [1] steps per share, written by block 0 for the join
-    int64_t* base;                          // [S] first step of each request
+    int* share;                             // [1] steps per share, written by block 0 for the join
+    int* base;                              // [S] first step of each request
     float* part;                            // [2 shares][rows][D] unnormalised sums
     float2* ml;                             // [2 shares][rows] (maximum, sum)
 };
@@ -84,9 +87,10 @@ struct Request {
     int row0, n, first;                     // first batch row, rows, position of its first row
     int len;                                // positions that the table can hold
     int units;                              // row groups * key-value heads
-    int steps;                              // steps of each of its units
+    int steps;                              // cost of each of its units, in steps
 };
-MOE_DEV Request request_of(const AttnArgs& a, int s, int rows_per_unit, int step_len) {
+template <int RB, int STEP>
+MOE_DEV Request request_of(const AttnArgs& a, int s) {
     Request r;
     const int b = min(max(a.q_offsets[s], 0), a.T), e = min(max(a.q_offsets[s + 1], 0), a.T);
     const int L = max(a.kv_len[s], 0);
@@ -95,9 +99,8 @@ MOE_DEV Request request_of(const AttnArgs& a, int s, int rows_per_unit, int step
     r.first = L - r.n;
     r.len = (int)min((int64_t)L, (int64_t)a.W << a.kv.page_shift);
     const int lo = a.window > 0 ? max(r.first - a.window + 1, 0) : 0;
-    const int G = a.n_heads / a.kv.n_kv_heads;
-    r.units = (int)(((int64_t)r.n * G + rows_per_unit - 1) / rows_per_unit) * a.kv.n_kv_heads;
-    r.steps = max((int)(((int64_t)max(r.len - lo, 0) + step_len - 1) / step_len), 1);
+    r.units = (int)(((uint32_t)(r.n * a.G) + RB - 1) / RB) * a.kv.n_kv_heads;      // (T * n_heads fits int32)
+    r.steps = (max(r.len - lo, 0) + STEP - 1) / STEP + PIECE_COST;
     return r;
 }
 
@@ -126,6 +129,15 @@ MOE_DEV uint32_t buf32(rsrc_t r, int off) { return __builtin_amdgcn_raw_buffer_l
 // the page table through the scalar cache (nothing writes it while the kernel runs)
 typedef const __attribute__((address_space(4))) int32_t* table_ptr;
 
+// First element of four consecutive results c of a row as the second product
+// leaves them, (h, e, 4 g + i): elements 16 E h + E (4 g + i) + e, i = 0 .. 3.
+template <int D>
+MOE_DEV int dim_of(int c) {
+    constexpr int E = D == 64 ? 4 : 8;
+    const int g = c & 3, e = (c >> 2) % E, h = (c >> 2) / E;
+    return 16 * E * h + 4 * E * g + e;
+}
+
 // blocks per CU, by registers
 constexpr int blocks_per_cu(int D, int MT) { return MT == 1 || (D == 64 && MT == 2) ? 2 : 1; }
 constexpr int shares_of(int D, int MT) { return 256 * blocks_per_cu(D, MT); }
@@ -150,81 +162,71 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     constexpr int DP = D + 4;               // padded row of the join area
     constexpr int QP = D + 8;               // padded q row, bf16
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    // more than 64 requests: [S + 1] first steps; then the q rows / join area
+    // more than 64 requests: [S] first steps; then the q rows / join area
     const bool lanes = a.S <= WAVE;
-    int64_t* base = (int64_t*)smem;
-    unsigned char* area = smem + (lanes ? 0 : ((size_t)(a.S + 1) * 8 + 15) / 16 * 16);
+    int* base = (int*)smem;
+    unsigned char* area = smem + (lanes ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16);
     uint16_t* qs = (uint16_t*)area;                              // [RB][QP]
     float* ja = (float*)area;                                    // [NW][16][DP]
     float2* jml = (float2*)(area + sizeof(float) * NW * 16 * DP);  // [NW][16]
-    __shared__ int64_t sc64[NW];
+    __shared__ int sc32[NW];
     __shared__ int strange;                 // the piece met infinite or NaN values in a tile seen in part
 
     const int tid = threadIdx.x, l = lane_id(), w = __builtin_amdgcn_readfirstlane(tid / WAVE);
-    const int G = a.n_heads / a.kv.n_kv_heads, nkv = a.kv.n_kv_heads;
+    const int G = a.G, nkv = a.kv.n_kv_heads;
 
     // ---- first step of every request.  Up to 64 requests: lane s holds request
     // s, in every wave by itself.  More: running sums through LDS, 256 at a time.
     Request mine;
-    int64_t my_base = 0, total;
+    int my_base = 0, total;
     if (lanes) {
-        mine = request_of(a, min(l, a.S - 1), RB, STEP);
+        mine = request_of<RB, STEP>(a, min(l, a.S - 1));
         if (l >= a.S) mine.units = 0;
-        const int64_t c = (int64_t)mine.units * mine.steps;
-        int64_t incl = c;
-#pragma unroll
-        for (int d = 1; d < WAVE; d <<= 1) {
-            const int64_t o = __shfl_up(incl, d, WAVE);
-            if (l >= d) incl += o;
-        }
-        total = __shfl(incl, WAVE - 1, WAVE);
+        const int c = mine.units * mine.steps, incl = wave_incl_scan(c);
+        total = __builtin_amdgcn_readlane(incl, WAVE - 1);
         my_base = incl - c;
         if (blockIdx.x == 0 && w == 0 && l < a.S) a.base[l] = my_base;
     } else {
         total = 0;
         for (int s0 = 0; s0 < a.S; s0 += AT_THREADS) {
             const int s = s0 + tid;
-            int64_t c = 0;
+            int c = 0;
             if (s < a.S) {
-                const Request r = request_of(a, s, RB, STEP);
-                c = (int64_t)r.units * r.steps;
+                const Request r = request_of<RB, STEP>(a, s);
+                c = r.units * r.steps;
             }
-            int64_t incl = c;
-#pragma unroll
-            for (int d = 1; d < WAVE; d <<= 1) {
-                const int64_t o = __shfl_up(incl, d, WAVE);
-                if (l >= d) incl += o;
-            }
+            const int incl = wave_incl_scan(c);
             __syncthreads();                // the scratch's last readers are done
-            if (l == WAVE - 1) sc64[w] = incl;
+            if (l == WAVE - 1) sc32[w] = incl;
             __syncthreads();
-            int64_t b = total;
+            int b = total;
 #pragma unroll
             for (int i = 0; i < NW; i++) {
-                if (i < w) b += sc64[i];
-                total += sc64[i];
+                if (i < w) b += sc32[i];
+                total += sc32[i];
             }
             if (s < a.S) {
                 base[s] = b + incl - c;
                 if (blockIdx.x == 0) a.base[s] = b + incl - c;
             }
         }
-        if (tid == 0) base[a.S] = total;
         __syncthreads();
+        total = __builtin_amdgcn_readfirstlane(total);
     }
-    const int64_t share = max((total + a.shares - 1) / a.shares, (int64_t)1);
+    const int share = max((int)(((uint32_t)total + a.shares - 1) / a.shares), 1);
     if (blockIdx.x == 0 && tid == 0) a.share[0] = share;
-    const int64_t share_lo = blockIdx.x * share, share_hi = min(share_lo + share, total);
+    const int share_lo = min((int64_t)blockIdx.x * share, (int64_t)total);
+    const int share_hi = min((int64_t)share_lo + share, (int64_t)total);
 
     const int r16 = l & 15, g4 = l >> 4;
     const float qscale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * LOG2E;
     const float capk = a.softcap * LOG2E;
     const int ps = a.kv.page_shift, pmask = (1 << ps) - 1;
 
-    for (int64_t at = share_lo; at < share_hi;) {
+    for (int at = share_lo; at < share_hi;) {
         int s;
         Request rq;
-        int64_t s_base;
+        int s_base;
         if (lanes) {
             s = __popcll(__ballot(l < a.S && my_base <= at)) - 1;      // (empty requests share a base with their successor)
             rq.row0 = __builtin_amdgcn_readlane(mine.row0, s);
@@ -233,8 +235,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             rq.len = __builtin_amdgcn_readlane(mine.len, s);
             rq.units = __builtin_amdgcn_readlane(mine.units, s);
             rq.steps = __builtin_amdgcn_readlane(mine.steps, s);
-            s_base = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_base, s) |
-                     ((int64_t)__builtin_amdgcn_readlane((int)(my_base >> 32), s) << 32);
+            s_base = __builtin_amdgcn_readlane(my_base, s);
         } else {
             s = 0;
             int hi = a.S;
@@ -244,18 +245,28 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                 else hi = mid;
             }
             s = __builtin_amdgcn_readfirstlane(s);
-            rq = request_of(a, s, RB, STEP);
+            rq = request_of<RB, STEP>(a, s);
             s_base = base[s];
         }
+        // (the same in every lane, and kept in scalar registers: buffer descriptors
+        // made from vector registers cost a loop around each load)
+        s = uniform(s);
+        s_base = uniform(s_base);
+        rq.row0 = uniform(rq.row0);
+        rq.n = uniform(rq.n);
+        rq.first = uniform(rq.first);
+        rq.len = uniform(rq.len);
+        rq.steps = uniform(rq.steps);
         // the piece: steps [st0, st1) of unit (row group, head)
-        const int unit = (int)((at - s_base) / rq.steps);
-        const int st0 = (int)(at - s_base - (int64_t)unit * rq.steps);
-        const int st1 = (int)min((int64_t)rq.steps, st0 + (share_hi - at));
-        const int64_t piece_at = at;
+        const int unit = uniform((int)((uint32_t)(at - s_base) / (uint32_t)rq.steps));
+        const int st0 = at - s_base - unit * rq.steps;
+        const int st1 = min(rq.steps, st0 + (share_hi - at));
+        const int piece_at = at;
         at += st1 - st0;
-        const int grp = unit / nkv, head = unit - grp * nkv;
+        const int grp = uniform((int)((uint32_t)unit / (uint32_t)nkv)), head = unit - grp * nkv;
         const int row0 = grp * RB, nrows = min(RB, rq.n * G - row0);
-        const int i0 = row0 / G, i1 = (row0 + nrows - 1) / G;
+        const int i0 = (int)((uint32_t)row0 / (uint32_t)G), r_in = row0 - i0 * G;   // row0 = token i0, its head r_in
+        const int i1 = i0 + (((r_in + nrows - 1) * a.G16) >> 16);
         // positions [see_lo, see_hi) that some row of the unit sees; the piece's
         // steps are its share of them (units of a request have equally many
         // steps, though the first rows of a long prompt see less)
@@ -264,8 +275,12 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         const int see_hi = max(min(p_hi + 1, rq.len), 0);
         const int a0 = see_lo & ~(TILE - 1);
         const int real_steps = (max(see_hi - a0, 0) + STEP - 1) / STEP;
-        const int t_lo = min((int64_t)a0 + (int64_t)real_steps * st0 / rq.steps * STEP, (int64_t)see_hi);
-        const int t_hi = min((int64_t)a0 + (int64_t)real_steps * st1 / rq.steps * STEP, (int64_t)see_hi);
+        const float stretch = (float)real_steps / (float)rq.steps;
+        auto step_at = [&](int st) {        // monotone in st, whole at the end: neighbouring pieces meet
+            return st == rq.steps || real_steps == rq.steps ? min(st, real_steps) : min((int)((float)st * stretch), real_steps);
+        };
+        const int t_lo = uniform((int)min((int64_t)a0 + (int64_t)step_at(st0) * STEP, (int64_t)see_hi));
+        const int t_hi = uniform(st1 == rq.steps ? see_hi : (int)min((int64_t)a0 + (int64_t)step_at(st1) * STEP, (int64_t)see_hi));
         // every row sees [full_lo, full_hi) whole
         const int full_lo = a.window > 0 ? max(p_hi - a.window + 1, 0) : 0;
         const int full_hi = min(p_lo + 1, rq.len);
@@ -278,7 +293,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
 #pragma unroll
             for (int sb = 0; sb < NSUB; sb++) {
                 const int v = trow[min((t0 + 16 * sb) >> ps, a.W - 1)];
-                e.p[sb] = (v >= 0 && v < a.kv.num_pages && t0 < t_hi) ? v : -1;
+                e.p[sb] = uniform((v >= 0 && v < a.kv.num_pages && t0 < t_hi) ? v : -1);
             }
             return e;
         };
@@ -331,15 +346,27 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         auto q_dim = [&](int k) __attribute__((always_inline)) {
             return F8 ? 16 * (4 * (k >> 1) + g4) + 8 * (k & 1) : 32 * k + 8 * g4;
         };
+        auto q_row = [&](int rr) __attribute__((always_inline)) -> const uint16_t* {
+            const int x = r_in + min(rr, nrows - 1);            // (rows past the unit's repeat its last, unused)
+            const int i = (x * a.G16) >> 16, g = x - i * G;
+            return a.q + (int64_t)(rq.row0 + i0 + i) * a.q_stride + (int64_t)(head * G + g) * D;
+        };
+        // the loads go out before the first tile's: they are waited for first
+        constexpr int QN = QREG ? 1 : RB * (D / 8) / AT_THREADS;
         bf16x8_t qf[QREG ? MT : 1][QREG ? D / 32 : 1];
+        u32x4_a qv[QN];
         if constexpr (QREG) {
 #pragma unroll
             for (int mt = 0; mt < MT; mt++) {
-                const int rr = min(mt * 16 + r16, nrows - 1);        // (rows past the unit's repeat its last, unused)
-                const int row = row0 + rr, i = row / G, g = row - i * G;
-                const uint16_t* src = a.q + (int64_t)(rq.row0 + i) * a.q_stride + (int64_t)(head * G + g) * D;
+                const uint16_t* src = q_row(mt * 16 + r16);
 #pragma unroll
                 for (int k = 0; k < D / 32; k++) qf[mt][k] = *reinterpret_cast<const bf16x8_t*>(src + q_dim(k));
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < QN; n++) {
+                const int c = n * AT_THREADS + tid;
+                qv[n] = *reinterpret_cast<const u32x4_a*>(q_row(c / (D / 8)) + c % (D / 8) * 8);
             }
         }
         TL t;
@@ -347,17 +374,16 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         Pages pg = pages_of(t_first), pg_next = pages_of(t_first + STEP);
         load_k(t, t_first, pg);
         load_v(t, t_first, pg);
-        __syncthreads();                    // the last piece's join area is read
+        lds_barrier();                      // the last piece's join area is read
         if (tid == 0) strange = 0;
         if constexpr (!QREG) {
-            for (int c = tid; c < RB * (D / 8); c += AT_THREADS) {
-                const int rr = c / (D / 8), cc = c - rr * (D / 8);
-                const int row = row0 + min(rr, nrows - 1), i = row / G, g = row - i * G;
-                *reinterpret_cast<uint4*>(qs + rr * QP + cc * 8) = *reinterpret_cast<const uint4*>(
-                    a.q + (int64_t)(rq.row0 + i) * a.q_stride + (int64_t)(head * G + g) * D + cc * 8);
+#pragma unroll
+            for (int n = 0; n < QN; n++) {
+                const int c = n * AT_THREADS + tid;
+                *reinterpret_cast<u32x4_a*>(qs + c / (D / 8) * QP + c % (D / 8) * 8) = qv[n];
             }
         }
-        __syncthreads();
+        lds_barrier();
         auto q_frag = [&](int mt, int k) __attribute__((always_inline)) {
             if constexpr (QREG) return qf[mt][k];
             else return *reinterpret_cast<const bf16x8_t*>(qs + (mt * 16 + r16) * QP + q_dim(k));
@@ -366,8 +392,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         int vlo[MT], vhi[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            const int i = (row0 + mt * 16 + r16) / G;
-            const int p = rq.first + i;
+            const int p = rq.first + i0 + (((r_in + mt * 16 + r16) * a.G16) >> 16);
             vhi[mt] = mt * 16 + r16 < nrows ? min(p, rq.len - 1) : -1;
             vlo[mt] = a.window > 0 ? max(p - a.window + 1, 0) : 0;
         }
@@ -469,15 +494,16 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             top = fmaxf(top, tr_partner<32>(top));
             const float mn = fmaxf(m[mt], top);
             const float base2 = mn == -__builtin_inff() ? 0.f : mn;      // a row that has seen nothing yet
-            if (__any(mn > m[mt])) {
+            // (nothing to scale before the first tile that a row sees)
+            if (__any(mn > m[mt] && m[mt] > -__builtin_inff())) {
                 const float f = __builtin_amdgcn_exp2f(m[mt] - base2);
                 sum[mt] *= f;
 #pragma unroll
                 for (int h = 0; h < NH; h++)
 #pragma unroll
                     for (int e = 0; e < E; e++) acc[mt][h][e] *= f;
-                m[mt] = mn;
             }
+            m[mt] = mn;
 #pragma unroll
             for (int sb = 0; sb < NSUB; sb++)
 #pragma unroll
@@ -600,9 +626,9 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             }
             return true;
         };
-        // the infinite and NaN values left out above, of elements d .. d + 3 and the
-        // positions that a row at position p sees (every probability is > 0)
-        auto add_strange = [&](f32x4_t& o, int p, int d) {
+        // the infinite and NaN values left out above, of elements d + {0, 1, 2, 3} sd
+        // and the positions that a row at position p sees (every probability is > 0)
+        auto add_strange = [&](f32x4_t& o, int p, int d, int sd) {
             for (int t0 = t_lo; t0 < t_hi; t0 += TILE) {
                 if (whole_tile(t0)) continue;
                 for (int pos = max(t0, a.window > 0 ? p - a.window + 1 : 0); pos < min(t0 + TILE, min(p + 1, see_hi)); pos++) {
@@ -612,9 +638,9 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         if constexpr (F8) {
-                            if ((((const uint8_t*)a.kv.v)[at + c] & 0x7F) == 0x7F) o[c] = __builtin_nanf("");
+                            if ((((const uint8_t*)a.kv.v)[at + c * sd] & 0x7F) == 0x7F) o[c] = __builtin_nanf("");
                         } else {
-                            const uint16_t v = ((const uint16_t*)a.kv.v)[at + c];
+                            const uint16_t v = ((const uint16_t*)a.kv.v)[at + c * sd];
                             if ((v & 0x7F80) == 0x7F80) o[c] += bf16_to_f32(v);
                         }
                     }
@@ -625,27 +651,29 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         // ---- join the block's waves, one row tile at a time.  A unit that lies in
         // this share alone is done; of others the piece that begins with the share
         // is partial 2 b, one that begins inside it 2 b + 1.
+        // (The loop stays a loop: code that runs once per piece is paid for in
+        // instruction fetches, about 60 ns per 64 bytes.)
         const bool direct = st1 - st0 == rq.steps;
         const int64_t pidx = 2 * (int64_t)blockIdx.x + (piece_at == share_lo ? 0 : 1);
-#pragma unroll
+#pragma unroll 1
         for (int mt = 0; mt < MT; mt++) {
-            float sm = sum[mt];
-            sm += tr_partner<16>(sm);
-            sm += tr_partner<32>(sm);
-            if (mt > 0 || !QREG) __syncthreads();   // the row tile before, or the q rows, are read
-            if (g4 == 0) jml[w * 16 + r16] = make_float2(m[mt], sm);
-            // lane: row r16; O^T rows 4 g4 + i of MFMA e are d = 16 E h + E (4 g4 + i) + e
+            if (mt > 0 || !QREG) lds_barrier();     // the row tile before, or the q rows, are read
 #pragma unroll
-            for (int h = 0; h < NH; h++)
+            for (int k = 0; k < MT; k++) {
+                if (mt != k) continue;              // uniform
+                float sm = sum[k];
+                sm += tr_partner<16>(sm);
+                sm += tr_partner<32>(sm);
+                if (g4 == 0) jml[w * 16 + r16] = make_float2(m[k], sm);
+                // O^T rows 4 g4 + i of MFMA (h, e) are d = 16 E h + E (4 g4 + i) + e: kept
+                // in that order, (h, e, 4 g4 + i), here and in the partial results
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float* dst = ja + (w * 16 + r16) * DP + 16 * E * h + E * (4 * g4 + i);
+                for (int h = 0; h < NH; h++)
 #pragma unroll
-                    for (int e = 0; e < E; e += 4)
-                        *reinterpret_cast<f32x4_t*>(dst + e) =
-                            f32x4_t{acc[mt][h][e][i], acc[mt][h][e + 1][i], acc[mt][h][e + 2][i], acc[mt][h][e + 3][i]};
-                }
-            __syncthreads();
+                    for (int e = 0; e < E; e++)
+                        *reinterpret_cast<f32x4_t*>(ja + (w * 16 + r16) * DP + (h * E + e) * 16 + 4 * g4) = acc[k][h][e];
+            }
+            lds_barrier();
             // 16 threads per row, D / 16 elements each, 4 at a time
             const int rr = tid >> 4, part = tid & 15, row = mt * 16 + rr;
             if (row < nrows) {
@@ -661,22 +689,23 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                     f[i] = __builtin_amdgcn_exp2f(x[i].x - br);
                     L += x[i].y * f[i];
                 }
-                const float inv = L == 0.f ? 0.f : 1.0f / L;         // (a row that sees nothing: 0)
-                const int grow = row0 + row, i = grow / G, g = grow - i * G;
+                const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);     // (a row that sees nothing: 0)
+                const int x0 = r_in + row, i = i0 + ((x0 * a.G16) >> 16), g = x0 - (i - i0) * G;
                 uint16_t* dst = a.out + ((int64_t)(rq.row0 + i) * a.n_heads + head * G + g) * D;
                 float* pd = a.part + (pidx * RB + row) * D;
+                const int odd = strange;
+#pragma unroll 1
+                for (int c = part; c < D / 4; c += 16) {
+                    const float* src = ja + rr * DP + c * 4;
+                    f32x4_t o = *reinterpret_cast<const f32x4_t*>(src) * f[0];
 #pragma unroll
-                for (int c = 0; c < D / 64; c++) {
-                    const int d = c * 64 + part * 4;
-                    f32x4_t o = *reinterpret_cast<const f32x4_t*>(ja + rr * DP + d) * f[0];
-#pragma unroll
-                    for (int i2 = 1; i2 < NW; i2++) o += *reinterpret_cast<const f32x4_t*>(ja + (i2 * 16 + rr) * DP + d) * f[i2];
-                    if (strange) add_strange(o, rq.first + i, d);
+                    for (int i2 = 1; i2 < NW; i2++) o += *reinterpret_cast<const f32x4_t*>(src + i2 * 16 * DP) * f[i2];
+                    if (odd) add_strange(o, rq.first + i, dim_of<D>(c), E);
                     if (direct) {
-                        const u32x2_a q = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
-                        *reinterpret_cast<u32x2_a*>(dst + d) = q;
+#pragma unroll
+                        for (int q = 0; q < 4; q++) dst[dim_of<D>(c) + E * q] = (uint16_t)pk_bf16(o[q] * inv, 0.f);
                     } else {
-                        *reinterpret_cast<f32x4_t*>(pd + d) = o;
+                        *reinterpret_cast<f32x4_t*>(pd + c * 4) = o;
                     }
                 }
                 if (!direct && part == 0) a.ml[pidx * RB + row] = make_float2(Mr, L);
@@ -693,31 +722,34 @@ __global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
     constexpr int NC = D / 64, NG = AT_THREADS / 16;
     __shared__ float2 gml[NG];
     __shared__ f32x4_t go[NG][16];
-    const int c = blockIdx.x % NC;
-    const int64_t id = blockIdx.x / NC;
-    const int t = (int)(id / a.n_heads), hq = (int)(id - (int64_t)t * a.n_heads);
+    const int t = blockIdx.x, hq = blockIdx.y / NC, c = blockIdx.y % NC;
     int s = 0, hi = a.S;
     while (hi - s > 1) {
         const int mid = (s + hi) >> 1;
         if (a.q_offsets[mid] <= t) s = mid;
         else hi = mid;
     }
-    const Request rq = request_of(a, s, RB, STEP);
-    const int64_t share = a.share[0];
+    const Request rq = request_of<RB, STEP>(a, s);
+    const int share = a.share[0];
     if (t < rq.row0 || t >= rq.row0 + rq.n) return;
-    const int nkv = a.kv.n_kv_heads, G = a.n_heads / nkv;
+    const int nkv = a.kv.n_kv_heads, G = a.G;
     const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
     const int grp = row / RB, rr = row - grp * RB;
-    const int64_t u0 = a.base[s] + ((int64_t)grp * nkv + head) * rq.steps;    // the unit's first step
-    const int64_t b0 = u0 / share;
-    const int np = (int)((u0 + rq.steps - 1) / share - b0) + 1;
+    const int u0 = a.base[s] + (grp * nkv + head) * rq.steps;    // the unit's first step
+    // (at most shares - 1 <= 511: the fp32 quotient is off by one at most)
+    auto share_of = [&](int u) {
+        const int q = (int)((float)u * __builtin_amdgcn_rcpf((float)share));
+        return q + ((int64_t)(q + 1) * share <= u ? 1 : 0) - ((int64_t)q * share > u ? 1 : 0);
+    };
+    const int b0 = share_of(u0), np = share_of(u0 + rq.steps - 1) - b0 + 1;
     if (np <= 1) return;
     const int first_odd = u0 == b0 * share ? 0 : 1;
     const int e = threadIdx.x & 15, gr = threadIdx.x >> 4;
     float M = -__builtin_inff(), L = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int p = gr; p < np; p += NG) {
-        const int64_t at = (2 * (b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
+        const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
         const float2 x = a.ml[at];
         const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + at * D + c * 64 + e * 4);
         const float mn = fmaxf(M, x.x), base = mn == -__builtin_inff() ? 0.f : mn;
@@ -730,10 +762,12 @@ __global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
     go[gr][e] = o;
     __syncthreads();
     if (gr > 0) return;
+#pragma unroll 4
     for (int i = 0; i < NG; i++) M = fmaxf(M, gml[i].x);
     const float base = M == -__builtin_inff() ? 0.f : M;
     L = 0.f;
     o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int i = 0; i < NG; i++) {
         const float2 x = gml[i];
         const float f = __builtin_amdgcn_exp2f(x.x - base);
@@ -741,8 +775,9 @@ __global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
         o += go[i][e] * f;
     }
     const float inv = L == 0.f ? 0.f : 1.0f / L;
-    const u32x2_a q = {pk_bf16(o[0] * inv, o[1] * inv), pk_bf16(o[2] * inv, o[3] * inv)};
-    *reinterpret_cast<u32x2_a*>(a.out + ((int64_t)t * a.n_heads + hq) * D + c * 64 + e * 4) = q;
+    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c * 16 + e);
+#pragma unroll
+    for (int i = 0; i < 4; i++) dst[(D == 64 ? 4 : 8) * i] = (uint16_t)pk_bf16(o[i] * inv, 0.f);
 }
 
 // Row tiles per unit: as many as a request has rows on average, so that its
@@ -764,7 +799,7 @@ AttnWs attn_ws(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
     const int mt = row_tiles(T, n_heads, n_kv_heads, head_dim, S), rb = 16 * mt;
     const size_t parts = 2 * (size_t)shares_of(head_dim, mt);
     AttnWs w;
-    w.ml = up256(((size_t)S + 1) * sizeof(int64_t));
+    w.ml = up256(((size_t)S + 1) * sizeof(int));
     w.part = w.ml + up256(parts * rb * sizeof(float2));
     w.total = w.part + up256(parts * rb * head_dim * sizeof(float));
     return w;
@@ -774,7 +809,7 @@ template <int D, int F8, int MT>
 hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     using SH = Shape<D, F8, MT>;
     auto kern = k_paged_attn<D, F8, MT>;
-    const size_t head = a.S <= WAVE ? 0 : ((size_t)(a.S + 1) * 8 + 15) / 16 * 16;
+    const size_t head = a.S <= WAVE ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16;
     const size_t join = sizeof(float) * NW * 16 * (D + 4) + sizeof(float2) * NW * 16;
     const size_t qrows = SH::QREG ? 0 : (size_t)16 * MT * (D + 8) * 2;
     const size_t lds = head + (join > qrows ? join : qrows);
@@ -783,8 +818,8 @@ hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     if (e != hipSuccess) return e;
     a.shares = shares_of(D, MT);
     hipLaunchKernelGGL(kern, dim3(a.shares), dim3(AT_THREADS), lds, st, a);
-    const int64_t blocks = (int64_t)a.T * a.n_heads * (D / 64);
-    hipLaunchKernelGGL((k_attn_join<D, 16 * MT, 16 * SH::NSUB * NW>), dim3((unsigned)blocks), dim3(AT_THREADS), 0, st, a);
+    hipLaunchKernelGGL((k_attn_join<D, 16 * MT, 16 * SH::NSUB * NW>), dim3(a.T, a.n_heads * (D / 64)), dim3(AT_THREADS), 0,
+                       st, a);
     return hipGetLastError();
 }
 
@@ -816,7 +851,8 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     a.q = q; a.q_stride = q_stride; a.T = T; a.n_heads = n_heads; a.kv = cache;
     a.table = table; a.W = W; a.q_offsets = q_offsets; a.kv_len = kv_len; a.S = S;
     a.scale = scale; a.softcap = softcap; a.window = window; a.out = out;
-    a.share = (int64_t*)wb; a.base = (int64_t*)wb + 1;
+    a.share = (int*)wb; a.base = (int*)wb + 1;
+    a.G = n_heads / cache.n_kv_heads; a.G16 = (65536 + a.G - 1) / a.G;
     a.ml = (float2*)(wb + L.ml); a.part = (float*)(wb + L.part);
     const int mt = row_tiles(T, n_heads, cache.n_kv_heads, cache.head_dim, S);
     const bool f8 = cache.k_scale != nullptr;
