@@ -426,7 +426,7 @@ moe_status moe_qk_norm_rope(const void* qkv, int32_t x_dtype, int64_t qkv_stride
  * kernel, in a fixed order: the result does not vary from run to run.
  * Unsupported: q_dtype other than MOE_BF16; S > 4096; n_heads not a multiple of
  * n_kv_heads, or n_heads / n_kv_heads > 64; q_stride not a multiple of 8;
- * n_heads head_dim / 64 > 65535; W * page_size > 2^30; (T n_heads / 16 + S n_kv_heads) (W page_size / 64 + 1)
+ * n_heads head_dim / 64 > 65535; W * page_size > 2^30; (T n_heads / 16 + S n_kv_heads) (W page_size / 32 + 9)
  * past int32. */
 size_t moe_paged_attn_workspace_size(int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t S);
 moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int32_t T, int32_t n_heads,
@@ -444,7 +444,8 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
  *            may alias residual (not x).
  *   act      silu z / (1 + e^-z); gelu z * Phi(z); its tanh form; relu max(z, 0).
  * Unsupported: x_dtype or w_dtype other than MOE_BF16; K not a multiple of 64;
- * N or x_stride not a multiple of 8. */
+ * N or x_stride not a multiple of 8; K or x_stride > 2^22;
+ * (T / 64 + 1) (N / 64 + 1) > 2^27. */
 typedef enum {
     MOE_ACT_NONE = 0,
     MOE_ACT_SILU = 1,

@@ -98,8 +98,8 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
     if (q_dtype != MOE_BF16 || S_ > MAX_REQUESTS || n_heads % kv.n_kv_heads != 0 ||
         n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)n_heads * kv.head_dim > 64 * 65535 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
         return MOE_ERR_UNSUPPORTED;
-    // the steps of all units (16 rows of a key-value head, 64 positions at least) are counted in int32
-    if ((((int64_t)T * n_heads + 15) / 16 + (int64_t)S_ * kv.n_kv_heads) * (((int64_t)W << kv.page_shift) / 64 + 1) > INT32_MAX)
+    // the steps of all units (16 rows of a key-value head, 32 positions at least) are counted in int32
+    if ((((int64_t)T * n_heads + 15) / 16 + (int64_t)S_ * kv.n_kv_heads) * (((int64_t)W << kv.page_shift) / 32 + 9) > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !aligned4(page_table) || !aligned4(q_offsets) || !aligned4(kv_len))
         return MOE_ERR_UNSUPPORTED;
@@ -124,6 +124,9 @@ moe_status moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const vo
         w_dtype < MOE_F32 || w_dtype > MOE_FP8_E4M3 || act < MOE_ACT_NONE || act > MOE_ACT_RELU)
         return MOE_ERR_INVALID_ARG;
     if (x_dtype != MOE_BF16 || w_dtype != MOE_BF16 || K % 64 != 0 || N % 8 != 0 || x_stride % 8 != 0)
+        return MOE_ERR_UNSUPPORTED;
+    // 32-bit byte offsets within a tile of 256 rows, and tiles (64 x 64 at least) counted in int32
+    if (K > 1 << 22 || x_stride > 1 << 22 || ((int64_t)T / 64 + 1) * ((int64_t)N / 64 + 1) > INT32_MAX / 16)
         return MOE_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) || !aligned16(out))
         return MOE_ERR_UNSUPPORTED;

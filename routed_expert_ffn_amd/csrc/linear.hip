@@ -2,17 +2,23 @@
 //
 //   out[t][n] = cast( act( sum_k x[t][k] w[n][k] + bias[n] ) + residual[t][n] )
 //
-// 64 x 64 output tiles, K steps of 64 through LDS, MFMA 16x16x32 bf16 with the
-// weight as its first operand, so a lane's four results are consecutive
-// outputs of one row.  Rows behind T and N are read as row 0 and not stored.
+// Two kernels.  Few rows (T <= 16): the weights are read once and that is the
+// time, so k_linear_rows streams them through registers.  More rows: tiles of x
+// and w through LDS, k_linear_tile.  Sums, bias, activation and residual in fp32,
+// one rounding at the end.
 #include "attn.h"
 #include "common.h"
+#include "device.h"
+
+#include <algorithm>
 
 namespace {
 
-constexpr int LT_THREADS = 256;
 typedef uint32_t u32x2_l __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_l __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_l __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_ptr;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_RELU = 4 };
 
@@ -30,75 +36,354 @@ MOE_DEV uint32_t pk(float lo, float hi) {
     const bf16x2_l v = {(__bf16)lo, (__bf16)hi};
     return __builtin_bit_cast(uint32_t, v);
 }
+MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// four consecutive outputs of row t from n on (n % 4 == 0, N % 8 == 0)
-template <int OB>
-MOE_DEV void finish4(f32x4_t z, int64_t t, int n, int N, const float* bias, int act, const void* residual, void* out) {
-    if (bias) z += *reinterpret_cast<const f32x4_t*>(bias + n);
+// ------------------------------------------------------------------ few rows
+// A block takes 4 RG weight rows, its 8 waves a share of k each: K is cut into
+// steps of 128, wave w takes steps w KS .. w KS + KS - 1 of every 8 KS.  One load
+// instruction of a wave is 4 rows x 128 k, 256 contiguous bytes a row: lane
+// (r, g) = (l & 15, l >> 4) holds row r >> 2, chunk (16 bytes) 4 g + (r & 3).  As the
+// MFMA's first operand that is a 16-row matrix whose row r holds the k of
+// part r & 3 only, so there is one MFMA per part p, with the matching x chunks
+// as its second operand, and of its 16 result rows those with r & 3 = p count:
+// in result element i = p of each lane, row g, token l & 15.  Three quarters of
+// the MFMA's work is thrown away, which costs nothing (T <= 16 leaves the matrix
+// cores idle), and in return the loads need neither LDS nor narrow rows.
+// All of a block's loads go out at once.
+constexpr int ROWS_MAX_T = 16;
+constexpr int RW = 8;                      // waves per block
+
+template <int RG, int KS, int OB>
+__global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __restrict__ x, int x_stride,
+                                                              const uint16_t* __restrict__ w, const float* __restrict__ bias,
+                                                              int act, const void* residual, int T, int N, int K,
+                                                              int rows_per_block, void* out) {
+    __shared__ float red[RW][RG][WAVE];
+    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), r = l & 15, g = l >> 4;
+    const int n0 = blockIdx.x * rows_per_block, rows = min(rows_per_block, N - n0);
+    const int kc = K / 8;                  // 16-byte chunks of a row
+    // (chunks and rows past the end read as 0 without touching memory)
+    const rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(w + (int64_t)n0 * K), 0, rows * K * 2, 0x00027000);
+    const rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, ((T - 1) * x_stride + K) * 2, 0x00027000);
+    const int chunk = 4 * g + (r & 3);
+    float val[RG];
 #pragma unroll
-    for (int i = 0; i < 4; i++) z[i] = activate(z[i], act);
-    const int64_t o = t * N + n;
-    if constexpr (OB) {
-        if (residual) {
-            const u32x2_l r = *reinterpret_cast<const u32x2_l*>((const uint16_t*)residual + o);
-            z += f32x4_t{bf16lo_to_f32(r[0]), bf16hi_to_f32(r[0]), bf16lo_to_f32(r[1]), bf16hi_to_f32(r[1])};
+    for (int i = 0; i < RG; i++) val[i] = 0.f;
+    for (int s0 = wv * KS; s0 * 16 < kc; s0 += RW * KS) {
+        u32x4_l xf[KS][4], wf[RG][KS];
+#pragma unroll
+        for (int s = 0; s < KS; s++)
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                const int c = (s0 + s) * 16 + 4 * g + p;
+                xf[s][p] = __builtin_bit_cast(u32x4_l, __builtin_amdgcn_raw_buffer_load_b128(
+                                                           xr, c < kc && r < T ? (r * x_stride + c * 8) * 2 : -16, 0, 0));
+            }
+#pragma unroll
+        for (int i = 0; i < RG; i++)
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                const int c = (s0 + s) * 16 + chunk, row = 4 * i + (r >> 2);
+                wf[i][s] = __builtin_bit_cast(u32x4_l, __builtin_amdgcn_raw_buffer_load_b128(
+                                                           wr, c < kc && row < rows ? (row * K + c * 8) * 2 : -16, 0, 2));
+            }
+#pragma unroll
+        for (int i = 0; i < RG; i++) {
+            f32x4_t acc[4];
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < KS; s++)
+                    acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wf[i][s]),
+                                                                     __builtin_bit_cast(bf16x8_t, xf[s][p]), acc[p], 0, 0, 0);
+            }
+            val[i] += (acc[0][0] + acc[1][1]) + (acc[2][2] + acc[3][3]);
         }
-        *reinterpret_cast<u32x2_l*>((uint16_t*)out + o) = u32x2_l{pk(z[0], z[1]), pk(z[2], z[3])};
-    } else {
-        if (residual) z += *reinterpret_cast<const f32x4_t*>((const float*)residual + o);
-        *reinterpret_cast<f32x4_t*>((float*)out + o) = z;
+    }
+#pragma unroll
+    for (int i = 0; i < RG; i++) red[wv][i][l] = val[i];
+    __syncthreads();
+    // thread: output (t, row), the rows of a token side by side
+    for (int id = threadIdx.x; id < T * rows; id += RW * WAVE) {
+        const int t = id / rows, row = id - t * rows;
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < RW; i++) z += red[i][row >> 2][(row & 3) * 16 + t];
+        const int n = n0 + row;
+        if (bias) z += bias[n];
+        z = activate(z, act);
+        const int64_t o = (int64_t)t * N + n;
+        if constexpr (OB) {
+            if (residual) z += bf16_to_f32(((const uint16_t*)residual)[o]);
+            ((uint16_t*)out)[o] = (uint16_t)pk(z, 0.f);
+        } else {
+            if (residual) z += ((const float*)residual)[o];
+            ((float*)out)[o] = z;
+        }
     }
 }
 
-template <int OB>
-__global__ __launch_bounds__(LT_THREADS) void k_linear(const uint16_t* __restrict__ x, int64_t x_stride,
-                                                       const uint16_t* __restrict__ w, const float* __restrict__ bias,
-                                                       int act, const void* residual, int T, int N, int K, void* out) {
-    constexpr int BT = 64, BN = 64, BK = 64, LR = BK + 8;       // padded LDS rows
-    __shared__ __attribute__((aligned(16))) uint16_t xs[BT * LR], ws[BN * LR];
-    const int n0 = blockIdx.x * BN;
-    const int64_t t0 = (int64_t)blockIdx.y * BT;
-    const int tid = threadIdx.x, l = lane_id(), wv = tid / WAVE;
-    const int wn = (wv & 1) * 32, wt = (wv >> 1) * 32;
-    f32x4_t acc[2][2];
+// ------------------------------------------------------------------ many rows
+// BT x BN output tiles, K steps of BK through ST LDS stages filled by the LDS DMA
+// (16 bytes a lane), ST - 1 steps ahead: a stage is waited for ST - 2 steps after
+// its loads went out.  Four waves in 2 x 2, MFMA 32x32x16 with the weight as the
+// first operand, so a lane's results are runs of 4 consecutive outputs of one
+// row.  The fragments of the next K step are read from LDS under the MFMAs of the
+// current one, in two register sets.
+//   LDS rows are BK elements; their 16-byte chunks are swizzled (on the global
+// side of the DMA) so that 8 rows' reads of one chunk fall into 8 different
+// bank groups: BK 64 (128-byte rows): chunk ^ (row & 7); BK 32 (two rows per
+// 128 bytes): chunk ^ ((row >> 1) & 3).
+//   Blocks: tiles of one XCD (block mod 8) are neighbours, in panels of 8 column
+// tiles, so that they share x and w in its L2.
+constexpr int TILE_THREADS = 256;
+
+template <int N>
+MOE_DEV void wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+MOE_DEV void dma16(const void* g, lds_ptr* l) { __builtin_amdgcn_global_load_lds(g, l, 16, 0, 0); }
+
+template <int BT, int BN, int BK, int ST>
+struct TileGeo {
+    static constexpr int WT = BT / 2, WNC = BN / 2;          // a wave's rows and columns
+    static constexpr int IT = WT / 32, JT = WNC / 32;        // its MFMA tiles
+    static constexpr int ROWB = BK * 2;                      // LDS row bytes
+    static constexpr int STAGE = (BT + BN) * ROWB;
+    static constexpr int RPI = 1024 / ROWB;                  // rows per DMA instruction (1 KB)
+    static constexpr int DX = BT / RPI / 4, DW = BN / RPI / 4, DMA = DX + DW;   // per wave
+    static_assert(DX * RPI * 4 == BT && DW * RPI * 4 == BN, "whole DMA instructions per wave");
+    // epilogue: 32 rows x WNC columns fp32 per wave, rows padded by 16 bytes
+    static constexpr int EROW = WNC * 4 + 16, EPI = 4 * 32 * EROW;
+    static constexpr int LDS = STAGE * ST > EPI ? STAGE * ST : EPI;
+};
+
+template <int BT, int BN, int BK, int ST, int OB, int BPC>
+__global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_t* __restrict__ x, int x_stride,
+                                                                   const uint16_t* __restrict__ w,
+                                                                   const float* __restrict__ bias, int act,
+                                                                   const void* residual, int T, int N, int K, int tiles_t,
+                                                                   int tiles_n, void* out) {
+    using G = TileGeo<BT, BN, BK, ST>;
+    constexpr int IT = G::IT, JT = G::JT, KQ = BK / 16;      // MFMA steps per K step
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), wt = wv >> 1, wn = wv & 1;
+    // tile of this block
+    const int tiles = tiles_t * tiles_n, per = (tiles + 7) / 8;
+    const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return;
+    constexpr int PN = 8;
+    const int panel = id / (tiles_t * PN), pw = min(PN, tiles_n - panel * PN), in = id - panel * tiles_t * PN;
+    const int64_t t0 = (int64_t)(in / pw) * BT;
+    const int n0 = (panel * PN + in % pw) * BN;
+    const int rows_t = (int)min((int64_t)BT, T - t0), rows_n = min(BN, N - n0);
+
+    // DMA: lane -> row l / CPR of the instruction's rows, LDS chunk l % CPR, which
+    // holds global chunk (l % CPR) ^ swizzle(row).  Rows past the end repeat the last.
+    constexpr int CPR = G::ROWB / 16;
+    auto swz = [](int row) __attribute__((always_inline)) { return BK == 64 ? row & 7 : (row >> 1) & 3; };
+    const unsigned char* xb = (const unsigned char*)(x + t0 * x_stride);
+    const unsigned char* wb = (const unsigned char*)(w + (int64_t)n0 * K);
+    uint32_t xo[G::DX], wo[G::DW];
 #pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 < K; k0 += BK) {
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-            const int q = c * LT_THREADS + tid, r = q >> 3, ch = q & 7;
-            const int64_t t = t0 + r < T ? t0 + r : 0;
-            const int64_t n = n0 + r < N ? n0 + r : 0;
-            *reinterpret_cast<uint4*>(xs + r * LR + ch * 8) = *reinterpret_cast<const uint4*>(x + t * x_stride + k0 + ch * 8);
-            *reinterpret_cast<uint4*>(ws + r * LR + ch * 8) = *reinterpret_cast<const uint4*>(w + n * K + k0 + ch * 8);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < BK; kk += 32) {
-            bf16x8_t a[2], b[2];
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                a[i] = *reinterpret_cast<const bf16x8_t*>(ws + (wn + i * 16 + (l & 15)) * LR + kk + (l >> 4) * 8);
-                b[i] = *reinterpret_cast<const bf16x8_t*>(xs + (wt + i * 16 + (l & 15)) * LR + kk + (l >> 4) * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-        }
+    for (int i = 0; i < G::DX; i++) {
+        const int r = (wv * G::DX + i) * G::RPI + l / CPR;
+        xo[i] = (uint32_t)min(r, rows_t - 1) * (uint32_t)(x_stride * 2) + (uint32_t)(((l % CPR) ^ swz(r)) * 16);
     }
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < G::DW; i++) {
+        const int r = (wv * G::DW + i) * G::RPI + l / CPR;
+        wo[i] = (uint32_t)min(r, rows_n - 1) * (uint32_t)(K * 2) + (uint32_t)(((l % CPR) ^ swz(r)) * 16);
+    }
+    const int nk = K / BK;
+    auto issue = [&](int k) __attribute__((always_inline)) {
+        unsigned char* st = smem + (k % ST) * G::STAGE;
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
-            const int64_t t = t0 + wt + j * 16 + (l & 15);
-            const int n = n0 + wn + i * 16 + (l >> 4) * 4;
-            if (t < T && n < N) finish4<OB>(acc[i][j], t, n, N, bias, act, residual, out);
+        for (int i = 0; i < G::DX; i++) dma16(xb + (int64_t)k * G::ROWB + xo[i], (lds_ptr*)(st + (wv * G::DX + i) * 1024));
+#pragma unroll
+        for (int i = 0; i < G::DW; i++)
+            dma16(wb + (int64_t)k * G::ROWB + wo[i], (lds_ptr*)(st + BT * G::ROWB + (wv * G::DW + i) * 1024));
+    };
+    const int fr = l & 31, fh = l >> 5;
+    struct Frag { bf16x8_t x[IT][KQ], w[JT][KQ]; };
+    auto read = [&](Frag& f, int k) __attribute__((always_inline)) {
+        const unsigned char* st = smem + (k % ST) * G::STAGE;
+#pragma unroll
+        for (int q = 0; q < KQ; q++) {
+            const int c = q * 2 + fh;
+#pragma unroll
+            for (int i = 0; i < IT; i++) {
+                const int r = wt * G::WT + i * 32 + fr;
+                f.x[i][q] = *reinterpret_cast<const bf16x8_t*>(st + r * G::ROWB + ((c ^ swz(r)) * 16));
+            }
+#pragma unroll
+            for (int j = 0; j < JT; j++) {
+                const int r = wn * G::WNC + j * 32 + fr;
+                f.w[j][q] = *reinterpret_cast<const bf16x8_t*>(st + BT * G::ROWB + r * G::ROWB + ((c ^ swz(r)) * 16));
+            }
         }
+    };
+    f32x16_t acc[IT][JT];
+#pragma unroll
+    for (int i = 0; i < IT; i++)
+#pragma unroll
+        for (int j = 0; j < JT; j++)
+#pragma unroll
+            for (int v = 0; v < 16; v++) acc[i][j][v] = 0.f;
+    auto mma = [&](const Frag& f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < KQ; q++)
+#pragma unroll
+            for (int i = 0; i < IT; i++)
+#pragma unroll
+                for (int j = 0; j < JT; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.w[j][q], f.x[i][q], acc[i][j], 0, 0, 0);
+    };
+    // One K step: stage k + 1 has landed everywhere (each wave waits for its own
+    // loads, then the barrier); stage k - 1, read one step earlier still, is free
+    // for step k + ST - 1; the next fragments are read under this step's MFMAs.
+    auto step = [&](int k, Frag& cur, Frag& nxt) __attribute__((always_inline)) {
+        const int left = nk - 1 - k;                          // steps after this one
+        if (left >= ST - 2) wait_vm<G::DMA * (ST - 3)>();
+        else wait_vm<0>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (left >= ST - 1) issue(k + ST - 1);
+        if (left >= 1) read(nxt, k + 1);
+        mma(cur);
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; s++)
+        if (s < nk) issue(s);
+    Frag f0, f1;
+    if (nk >= ST - 1) wait_vm<G::DMA * (ST - 2)>();
+    else wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read(f0, 0);
+    int k = 0;
+    for (; k + 1 < nk; k += 2) {
+        step(k, f0, f1);
+        step(k + 1, f1, f0);
+    }
+    if (k < nk) mma(f0);
+
+    // ---- epilogue: 32 rows of the wave's tile at a time through its part of the
+    // LDS, then 8 consecutive outputs a lane
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();                             // every wave has read its last fragments
+    asm volatile("" ::: "memory");
+    unsigned char* ep = smem + wv * 32 * G::EROW;
+#pragma unroll 1
+    for (int i = 0; i < IT; i++) {
+#pragma unroll
+        for (int q = 0; q < IT; q++) {
+            if (i != q) continue;                             // uniform
+#pragma unroll
+            for (int j = 0; j < JT; j++)
+#pragma unroll
+                for (int v = 0; v < 4; v++)
+                    *reinterpret_cast<f32x4_t*>(ep + fr * G::EROW + (j * 32 + v * 8 + fh * 4) * 4) =
+                        f32x4_t{acc[q][j][4 * v], acc[q][j][4 * v + 1], acc[q][j][4 * v + 2], acc[q][j][4 * v + 3]};
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int LPR = G::WNC / 8, RPP = WAVE / LPR;     // lanes per row, rows per pass
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += RPP) {
+            const int r = r0 + l / LPR, c = l % LPR * 8;
+            const int64_t t = t0 + wt * G::WT + i * 32 + r;
+            const int n = n0 + wn * G::WNC + c;
+            f32x4_t z[2];
+            z[0] = *reinterpret_cast<const f32x4_t*>(ep + r * G::EROW + c * 4);
+            z[1] = *reinterpret_cast<const f32x4_t*>(ep + r * G::EROW + c * 4 + 16);
+            if (t >= T || n >= N) continue;
+            if (bias) {
+                z[0] += *reinterpret_cast<const f32x4_t*>(bias + n);
+                z[1] += *reinterpret_cast<const f32x4_t*>(bias + n + 4);
+            }
+            if (act != ACT_NONE)
+#pragma unroll 1
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) z[h][e] = activate(z[h][e], act);
+            const int64_t o = t * N + n;
+            if constexpr (OB) {
+                if (residual) {
+                    const u32x4_l q = *reinterpret_cast<const u32x4_l*>((const uint16_t*)residual + o);
+                    z[0] += f32x4_t{bf16lo_to_f32(q[0]), bf16hi_to_f32(q[0]), bf16lo_to_f32(q[1]), bf16hi_to_f32(q[1])};
+                    z[1] += f32x4_t{bf16lo_to_f32(q[2]), bf16hi_to_f32(q[2]), bf16lo_to_f32(q[3]), bf16hi_to_f32(q[3])};
+                }
+                *reinterpret_cast<u32x4_l*>((uint16_t*)out + o) =
+                    u32x4_l{pk(z[0][0], z[0][1]), pk(z[0][2], z[0][3]), pk(z[1][0], z[1][1]), pk(z[1][2], z[1][3])};
+            } else {
+                if (residual) {
+                    z[0] += *reinterpret_cast<const f32x4_t*>((const float*)residual + o);
+                    z[1] += *reinterpret_cast<const f32x4_t*>((const float*)residual + o + 4);
+                }
+                *reinterpret_cast<f32x4_t*>((float*)out + o) = z[0];
+                *reinterpret_cast<f32x4_t*>((float*)out + o + 4) = z[1];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+struct LinearArgs {
+    const uint16_t* x;
+    int x_stride;
+    const uint16_t* w;
+    const float* bias;
+    int act;
+    const void* residual;
+    int T, N, K;
+    void* out;
+};
+
+template <int RG, int KS, int OB>
+hipError_t launch_rows(const LinearArgs& a, int rows_per_block, hipStream_t st) {
+    hipLaunchKernelGGL((k_linear_rows<RG, KS, OB>), dim3((a.N + rows_per_block - 1) / rows_per_block), dim3(RW * WAVE), 0,
+                       st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual, a.T, a.N, a.K, rows_per_block, a.out);
+    return hipGetLastError();
+}
+
+template <int KS, int OB>
+hipError_t launch_rows_k(const LinearArgs& a, hipStream_t st) {
+    // one block per CU while it has at most 32 rows
+    const int groups = (a.N + 3) / 4, rg = std::min(std::max((groups + 255) / 256, 1), 8);
+    if (rg == 1) return launch_rows<1, KS, OB>(a, 4, st);
+    if (rg == 2) return launch_rows<2, KS, OB>(a, 8, st);
+    if (rg <= 4) return launch_rows<4, KS, OB>(a, 4 * rg, st);
+    return launch_rows<8, KS, OB>(a, 4 * rg, st);
+}
+
+template <int BT, int BN, int BK, int ST, int BPC, int OB>
+hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
+    auto kern = k_linear_tile<BT, BN, BK, ST, OB, BPC>;
+    static LdsLimit lim;
+    constexpr int lds = TileGeo<BT, BN, BK, ST>::LDS;
+    hipError_t e = lim.ensure((const void*)kern, lds);
+    if (e != hipSuccess) return e;
+    const int tt = (a.T + BT - 1) / BT, tn = (a.N + BN - 1) / BN, per = (tt * tn + 7) / 8;
+    hipLaunchKernelGGL(kern, dim3(per * 8), dim3(TILE_THREADS), lds, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual,
+                       a.T, a.N, a.K, tt, tn, a.out);
+    return hipGetLastError();
+}
+
+template <int OB>
+hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
+    if (a.T <= ROWS_MAX_T) {
+        if (a.K <= 1024) return launch_rows_k<1, OB>(a, st);
+        if (a.K <= 2048) return launch_rows_k<2, OB>(a, st);
+        return launch_rows_k<4, OB>(a, st);
+    }
+    auto tiles = [&](int bt, int bn) { return (int64_t)((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
+    if (tiles(256, 256) >= 192) return launch_tile<256, 256, 32, 4, 1, OB>(a, st);
+    if (tiles(128, 128) >= 192) return launch_tile<128, 128, 32, 4, 2, OB>(a, st);
+    return launch_tile<64, 64, 64, 4, 2, OB>(a, st);
 }
 
 }  // namespace
@@ -113,8 +398,6 @@ hipError_t launch_linear(const uint16_t* x, int64_t x_stride, const uint16_t* w,
                          hipStream_t st) {
     (void)ws;
     if (T == 0) return hipSuccess;
-    const dim3 grid((N + 63) / 64, (T + 63) / 64);
-    if (out_bf16) hipLaunchKernelGGL((k_linear<1>), grid, dim3(LT_THREADS), 0, st, x, x_stride, w, bias, act, residual, T, N, K, out);
-    else hipLaunchKernelGGL((k_linear<0>), grid, dim3(LT_THREADS), 0, st, x, x_stride, w, bias, act, residual, T, N, K, out);
-    return hipGetLastError();
+    const LinearArgs a{x, (int)x_stride, w, bias, act, residual, T, N, K, out};
+    return out_bf16 ? launch_ob<1>(a, st) : launch_ob<0>(a, st);
 }

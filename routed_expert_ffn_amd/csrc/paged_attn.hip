@@ -56,9 +56,9 @@ MOE_DEV uint32_t fp8x2_bf16(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
-// What a piece costs besides its steps (its q rows, first loads and join), in
-// steps: short requests would otherwise pile up in few shares.
-constexpr int PIECE_COST = 2;
+// What a piece costs besides its own positions (its q rows, first loads and
+// join), in positions: short requests would otherwise pile up in few shares.
+constexpr int PIECE_COST = 256;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -100,19 +100,19 @@ MOE_DEV Request request_of(const AttnArgs& a, int s) {
     r.len = (int)min((int64_t)L, (int64_t)a.W << a.kv.page_shift);
     const int lo = a.window > 0 ? max(r.first - a.window + 1, 0) : 0;
     r.units = (int)(((uint32_t)(r.n * a.G) + RB - 1) / RB) * a.kv.n_kv_heads;      // (T * n_heads fits int32)
-    r.steps = (max(r.len - lo, 0) + STEP - 1) / STEP + PIECE_COST;
+    r.steps = (max(r.len - lo, 0) + STEP - 1) / STEP + PIECE_COST / STEP;
     return r;
 }
 
 // One wave's NSUB sub-tiles of 16 positions.
-template <int D, int F8, int NSUB>
+template <int D, int F8, int NSUB, int DS>
 struct Tile {
     static constexpr int KV = F8 ? D / 64 : D / 32;       // 16-byte key chunks per lane and sub-tile
     static constexpr int E = D == 64 ? 4 : 8;             // value elements per lane and load
     static constexpr int NH = D / (16 * E);               // loads per position
     static constexpr int EW = F8 ? E / 4 : E / 2;         // their 32-bit words
     u32x4_a k[NSUB][KV];
-    uint32_t v[4 * NSUB][NH][EW];
+    uint32_t v[4 * NSUB][NH / DS][EW];
     f32x4_t ks[NSUB], vs[NSUB];
 };
 
@@ -122,9 +122,12 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 MOE_DEV rsrc_t buffer_of(const void* base, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
 }
-MOE_DEV u32x4_a buf128(rsrc_t r, int off) { return __builtin_bit_cast(u32x4_a, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0)); }
-MOE_DEV u32x2_a buf64(rsrc_t r, int off) { return __builtin_bit_cast(u32x2_a, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0)); }
-MOE_DEV uint32_t buf32(rsrc_t r, int off) { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
+template <int AUX>
+MOE_DEV u32x4_a buf128(rsrc_t r, int off) { return __builtin_bit_cast(u32x4_a, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, AUX)); }
+template <int AUX>
+MOE_DEV u32x2_a buf64(rsrc_t r, int off) { return __builtin_bit_cast(u32x2_a, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, AUX)); }
+template <int AUX>
+MOE_DEV uint32_t buf32(rsrc_t r, int off) { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, AUX); }
 
 // the page table through the scalar cache (nothing writes it while the kernel runs)
 typedef const __attribute__((address_space(4))) int32_t* table_ptr;
@@ -139,14 +142,19 @@ MOE_DEV int dim_of(int c) {
 }
 
 // blocks per CU, by registers
-constexpr int blocks_per_cu(int D, int MT) { return MT == 1 || (D == 64 && MT == 2) ? 2 : 1; }
+constexpr int blocks_per_cu(int D, int MT) { return MT == 1 || D == 64 || (D == 128 && MT == 2) || (D == 256 && MT == 2) ? 2 : 1; }
 constexpr int shares_of(int D, int MT) { return 256 * blocks_per_cu(D, MT); }
 
 // A kernel's shape: row tiles, sub-tiles per wave step, blocks per CU.
 template <int D, int F8, int MT>
 struct Shape {
-    // 16 KB of cache in flight per wave (8 KB of e4m3), by registers
-    static constexpr int NSUB = D == 256 && (MT > 1 || !F8) ? 1 : 2;
+    // Head parts: at head_dim 256 with more than one row tile two waves share
+    // their positions (and compute their scores twice), each summing the values of
+    // half of the head: half the accumulators, and half the planes to join.
+    static constexpr int DS = D == 256 && MT > 1 ? 2 : 1;
+    // sub-tiles per wave step: 16 KB of cache in flight per wave (8 KB of e4m3), by registers
+    static constexpr int NSUB = D == 256 && !F8 ? 1 : 2;
+    static constexpr int STEP = 16 * NSUB * NW / DS;    // positions per block step
     static constexpr bool QREG = D * MT <= 128;     // q fragments in registers (up to 16 of them), else LDS at each use
 };
 
@@ -154,11 +162,12 @@ template <int D, int F8, int MT>
 __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_attn(const AttnArgs a) {
     constexpr int NSUB = Shape<D, F8, MT>::NSUB;
     constexpr bool QREG = Shape<D, F8, MT>::QREG;
-    using TL = Tile<D, F8, NSUB>;
-    constexpr int E = TL::E, NH = TL::NH, EW = TL::EW, KV = TL::KV;
+    constexpr int DS = Shape<D, F8, MT>::DS, PW = NW / DS, STEP = Shape<D, F8, MT>::STEP;
+    using TL = Tile<D, F8, NSUB, DS>;
+    constexpr int E = TL::E, NH = TL::NH / DS, EW = TL::EW, KV = TL::KV;
     constexpr int TILE = 16 * NSUB;         // positions per wave step
-    constexpr int STEP = TILE * NW;
     constexpr int RB = 16 * MT;             // rows per unit
+    constexpr int NT = MT == 1 ? 2 : 0;     // the cache is read once: non-temporal
     constexpr int DP = D + 4;               // padded row of the join area
     constexpr int QP = D + 8;               // padded q row, bf16
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -167,12 +176,13 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     int* base = (int*)smem;
     unsigned char* area = smem + (lanes ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16);
     uint16_t* qs = (uint16_t*)area;                              // [RB][QP]
-    float* ja = (float*)area;                                    // [NW][16][DP]
-    float2* jml = (float2*)(area + sizeof(float) * NW * 16 * DP);  // [NW][16]
+    float* ja = (float*)area;                                    // [PW][16][DP]
+    float2* jml = (float2*)(area + sizeof(float) * PW * 16 * DP);  // [PW][16]
     __shared__ int sc32[NW];
     __shared__ int strange;                 // the piece met infinite or NaN values in a tile seen in part
 
     const int tid = threadIdx.x, l = lane_id(), w = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    const int wp = w % PW, wd = w / PW;     // the wave's positions and head part
     const int G = a.G, nkv = a.kv.n_kv_heads;
 
     // ---- first step of every request.  Up to 64 requests: lane s holds request
@@ -306,9 +316,9 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                 const rsrc_t r = buffer_of((const char*)a.kv.k + (((ph * (D / X)) << ps) + off) * 16,
                                            pg.p[sb] < 0 ? 0 : ((D / X) << ps) * 16 - off * 16);
 #pragma unroll
-                for (int c = 0; c < KV; c++) t.k[sb][c] = buf128(r, (((4 * c + g4) << ps) + r16) * 16);
+                for (int c = 0; c < KV; c++) t.k[sb][c] = buf128<NT>(r, (((4 * c + g4) << ps) + r16) * 16);
                 if constexpr (F8)
-                    t.ks[sb] = __builtin_bit_cast(f32x4_t, buf128(buffer_of(a.kv.k_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
+                    t.ks[sb] = __builtin_bit_cast(f32x4_t, buf128<NT>(buffer_of(a.kv.k_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
             }
         };
         auto load_v = [&](TL& t, int t0, const Pages& pg) __attribute__((always_inline)) {
@@ -316,7 +326,8 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             for (int sb = 0; sb < NSUB; sb++) {
                 const int64_t ph = (int64_t)max(pg.p[sb], 0) * nkv + head;
                 const int off = (t0 + 16 * sb) & pmask;
-                const rsrc_t r = buffer_of((const char*)a.kv.v + ((ph << ps) + off) * D * ES, pg.p[sb] < 0 ? 0 : 16 * D * ES);
+                const rsrc_t r = buffer_of((const char*)a.kv.v + (((ph << ps) + off) * D + wd * (D / DS)) * ES,
+                                           pg.p[sb] < 0 ? 0 : (16 * D - wd * (D / DS)) * ES);
 #pragma unroll
                 for (int j = 0; j < 4; j++)
 #pragma unroll
@@ -324,19 +335,19 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                         const int at = (4 * g4 * D + r16 * E + j * D + h * 16 * E) * ES;
                         uint32_t* v = t.v[4 * sb + j][h];
                         if constexpr (EW == 4) {
-                            const u32x4_a q = buf128(r, at);
+                            const u32x4_a q = buf128<NT>(r, at);
 #pragma unroll
                             for (int i = 0; i < 4; i++) v[i % EW] = q[i];
                         } else if constexpr (EW == 2) {
-                            const u32x2_a q = buf64(r, at);
+                            const u32x2_a q = buf64<NT>(r, at);
                             v[0] = q[0];
                             v[1 % EW] = q[1];
                         } else {
-                            v[0] = buf32(r, at);
+                            v[0] = buf32<NT>(r, at);
                         }
                     }
                 if constexpr (F8)
-                    t.vs[sb] = __builtin_bit_cast(f32x4_t, buf128(buffer_of(a.kv.v_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
+                    t.vs[sb] = __builtin_bit_cast(f32x4_t, buf128<NT>(buffer_of(a.kv.v_scale + (ph << ps) + off, pg.p[sb] < 0 ? 0 : 64), g4 * 16));
             }
         };
 
@@ -370,7 +381,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             }
         }
         TL t;
-        const int t_first = t_lo + w * TILE;
+        const int t_first = t_lo + wp * TILE;
         Pages pg = pages_of(t_first), pg_next = pages_of(t_first + STEP);
         load_k(t, t_first, pg);
         load_v(t, t_first, pg);
@@ -664,28 +675,28 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                 float sm = sum[k];
                 sm += tr_partner<16>(sm);
                 sm += tr_partner<32>(sm);
-                if (g4 == 0) jml[w * 16 + r16] = make_float2(m[k], sm);
+                if (g4 == 0 && wd == 0) jml[wp * 16 + r16] = make_float2(m[k], sm);
                 // O^T rows 4 g4 + i of MFMA (h, e) are d = 16 E h + E (4 g4 + i) + e: kept
                 // in that order, (h, e, 4 g4 + i), here and in the partial results
 #pragma unroll
                 for (int h = 0; h < NH; h++)
 #pragma unroll
                     for (int e = 0; e < E; e++)
-                        *reinterpret_cast<f32x4_t*>(ja + (w * 16 + r16) * DP + (h * E + e) * 16 + 4 * g4) = acc[k][h][e];
+                        *reinterpret_cast<f32x4_t*>(ja + (wp * 16 + r16) * DP + ((wd * NH + h) * E + e) * 16 + 4 * g4) = acc[k][h][e];
             }
             lds_barrier();
             // 16 threads per row, D / 16 elements each, 4 at a time
             const int rr = tid >> 4, part = tid & 15, row = mt * 16 + rr;
             if (row < nrows) {
-                float2 x[NW];
+                float2 x[PW];
 #pragma unroll
-                for (int i = 0; i < NW; i++) x[i] = jml[i * 16 + rr];
-                float Mr = x[0].x, L = 0.f, f[NW];
+                for (int i = 0; i < PW; i++) x[i] = jml[i * 16 + rr];
+                float Mr = x[0].x, L = 0.f, f[PW];
 #pragma unroll
-                for (int i = 1; i < NW; i++) Mr = fmaxf(Mr, x[i].x);
+                for (int i = 1; i < PW; i++) Mr = fmaxf(Mr, x[i].x);
                 const float br = Mr == -__builtin_inff() ? 0.f : Mr;
 #pragma unroll
-                for (int i = 0; i < NW; i++) {
+                for (int i = 0; i < PW; i++) {
                     f[i] = __builtin_amdgcn_exp2f(x[i].x - br);
                     L += x[i].y * f[i];
                 }
@@ -699,7 +710,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                     const float* src = ja + rr * DP + c * 4;
                     f32x4_t o = *reinterpret_cast<const f32x4_t*>(src) * f[0];
 #pragma unroll
-                    for (int i2 = 1; i2 < NW; i2++) o += *reinterpret_cast<const f32x4_t*>(src + i2 * 16 * DP) * f[i2];
+                    for (int i2 = 1; i2 < PW; i2++) o += *reinterpret_cast<const f32x4_t*>(src + i2 * 16 * DP) * f[i2];
                     if (odd) add_strange(o, rq.first + i, dim_of<D>(c), E);
                     if (direct) {
 #pragma unroll
@@ -714,24 +725,37 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     }
 }
 
-// out = sum_c 2^{m_c - M} acc_c / sum_c 2^{m_c - M} sum_c over the shares that a
-// unit lies in.  One block per (batch row, head, 64 elements): 16 threads of 4
-// elements, the shares dealt to 16 groups of them, joined through LDS in order.
-template <int D, int RB, int STEP>
-__global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
-    constexpr int NC = D / 64, NG = AT_THREADS / 16;
-    __shared__ float2 gml[NG];
-    __shared__ f32x4_t go[NG][16];
-    const int t = blockIdx.x, hq = blockIdx.y / NC, c = blockIdx.y % NC;
-    int s = 0, hi = a.S;
-    while (hi - s > 1) {
-        const int mid = (s + hi) >> 1;
-        if (a.q_offsets[mid] <= t) s = mid;
-        else hi = mid;
+// The request that batch row t lies in, searched by a wave: 64 offsets at a time.
+MOE_DEV int request_with(const AttnArgs& a, int t) {
+    const int l = lane_id();
+    int s = 0, stride = 1;
+    while (stride * WAVE < a.S) stride *= WAVE;
+    for (; stride >= 1; stride /= WAVE) {
+        const int i = s + l * stride;
+        s += max(__popcll(__ballot(i < a.S && a.q_offsets[min(i, a.S - 1)] <= t)) - 1, 0) * stride;
     }
-    const Request rq = request_of<RB, STEP>(a, s);
+    return uniform(s);
+}
+
+// out = sum_c 2^{m_c - M} acc_c / sum_c 2^{m_c - M} sum_c over the shares c that a
+// unit lies in.  WPR waves per (batch row, head, CH elements): CH / 4 lanes of 4
+// elements each, the shares dealt to the groups of them in all WPR waves, joined
+// across lanes and then through LDS in order.  Few rows take CH 64 and 16 or 4
+// waves (a unit in hundreds of shares; one token over 262,144 positions: 11 us
+// with 4 waves, 6 with 16), many rows one wave each (most of them in one share,
+// with nothing to do).
+template <int D, int RB, int STEP, int CH, int WPR>
+__global__ __launch_bounds__(WPR == 1 ? AT_THREADS : WPR * WAVE) void k_attn_join(const AttnArgs a) {
+    constexpr int NC = D / CH, TC = CH / 4, GW = WAVE / TC, NG = GW * WPR;
+    constexpr int U = 4;                   // shares in flight per thread
+    __shared__ float2 gml[WPR];
+    __shared__ f32x4_t go[WPR][TC];
+    const int l = lane_id(), w = uniform(threadIdx.x / WAVE);
+    const int t = blockIdx.x, y = WPR == 1 ? blockIdx.y * NW + w : blockIdx.y, hq = y / NC, c0 = y % NC * TC;
     const int share = a.share[0];
-    if (t < rq.row0 || t >= rq.row0 + rq.n) return;
+    const int s = request_with(a, t);
+    const Request rq = request_of<RB, STEP>(a, s);
+    if (hq >= a.n_heads || t < rq.row0 || t >= rq.row0 + rq.n) return;
     const int nkv = a.kv.n_kv_heads, G = a.G;
     const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
     const int grp = row / RB, rr = row - grp * RB;
@@ -744,38 +768,61 @@ __global__ __launch_bounds__(AT_THREADS) void k_attn_join(const AttnArgs a) {
     const int b0 = share_of(u0), np = share_of(u0 + rq.steps - 1) - b0 + 1;
     if (np <= 1) return;
     const int first_odd = u0 == b0 * share ? 0 : 1;
-    const int e = threadIdx.x & 15, gr = threadIdx.x >> 4;
+    const int e = l % TC, gr = (WPR == 1 ? 0 : w * GW) + l / TC;
     float M = -__builtin_inff(), L = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int p = gr; p < np; p += NG) {
-        const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
-        const float2 x = a.ml[at];
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + at * D + c * 64 + e * 4);
-        const float mn = fmaxf(M, x.x), base = mn == -__builtin_inff() ? 0.f : mn;
-        const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(x.x - base);
-        L = L * f0 + x.y * f1;
-        o = o * f0 + v * f1;
+    auto add = [&](float m2, float l2, f32x4_t v2) __attribute__((always_inline)) {
+        const float mn = fmaxf(M, m2), base = mn == -__builtin_inff() ? 0.f : mn;
+        const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(m2 - base);
+        L = L * f0 + l2 * f1;
+        o = o * f0 + v2 * f1;
         M = mn;
+    };
+    for (int p0 = gr; p0 < np; p0 += NG * U) {
+        float2 x[U];
+        f32x4_t v[U];
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int p = min(p0 + i * NG, np - 1);
+            const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
+            x[i] = a.ml[at];
+            v[i] = *reinterpret_cast<const f32x4_t*>(a.part + at * D + (c0 + e) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            if (p0 + i * NG >= np) break;
+            add(x[i].x, x[i].y, v[i]);
+        }
     }
-    if (e == 0) gml[gr] = make_float2(M, L);
-    go[gr][e] = o;
-    __syncthreads();
-    if (gr > 0) return;
-#pragma unroll 4
-    for (int i = 0; i < NG; i++) M = fmaxf(M, gml[i].x);
-    const float base = M == -__builtin_inff() ? 0.f : M;
-    L = 0.f;
-    o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < NG; i++) {
-        const float2 x = gml[i];
-        const float f = __builtin_amdgcn_exp2f(x.x - base);
-        L += x.y * f;
-        o += go[i][e] * f;
+    // the wave's groups: every lane ends with the sum over them, taken in the
+    // same order (its own pair's lower group first)
+#pragma unroll
+    for (int d = TC; d < WAVE; d <<= 1) {
+        const bool low = (l & d) == 0;
+        const float m2 = wave_xor(M, d), l2 = wave_xor(L, d);
+        f32x4_t v2;
+#pragma unroll
+        for (int i = 0; i < 4; i++) v2[i] = wave_xor(o[i], d);
+        const float m1 = M, l1 = L;
+        const f32x4_t v1 = o;
+        M = low ? m1 : m2; L = low ? l1 : l2; o = low ? v1 : v2;
+        add(low ? m2 : m1, low ? l2 : l1, low ? v2 : v1);
     }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
-    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c * 16 + e);
+    if constexpr (WPR > 1) {
+        if (l < TC) go[w][l] = o;
+        if (l == 0) gml[w] = make_float2(M, L);
+        __syncthreads();
+        if (threadIdx.x >= TC) return;
+        M = -__builtin_inff();
+        L = 0.f;
+        o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = 0; i < WPR; i++) add(gml[i].x, gml[i].y, go[i][e]);
+    } else if (l >= TC) {
+        return;
+    }
+    const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);
+    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c0 + e);
 #pragma unroll
     for (int i = 0; i < 4; i++) dst[(D == 64 ? 4 : 8) * i] = (uint16_t)pk_bf16(o[i] * inv, 0.f);
 }
@@ -810,7 +857,7 @@ hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     using SH = Shape<D, F8, MT>;
     auto kern = k_paged_attn<D, F8, MT>;
     const size_t head = a.S <= WAVE ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16;
-    const size_t join = sizeof(float) * NW * 16 * (D + 4) + sizeof(float2) * NW * 16;
+    const size_t join = (sizeof(float) * 16 * (D + 4) + sizeof(float2) * 16) * (NW / SH::DS);
     const size_t qrows = SH::QREG ? 0 : (size_t)16 * MT * (D + 8) * 2;
     const size_t lds = head + (join > qrows ? join : qrows);
     static LdsLimit lim;
@@ -818,8 +865,11 @@ hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     if (e != hipSuccess) return e;
     a.shares = shares_of(D, MT);
     hipLaunchKernelGGL(kern, dim3(a.shares), dim3(AT_THREADS), lds, st, a);
-    hipLaunchKernelGGL((k_attn_join<D, 16 * MT, 16 * SH::NSUB * NW>), dim3(a.T, a.n_heads * (D / 64)), dim3(AT_THREADS), 0,
-                       st, a);
+    const int64_t chunks = (int64_t)a.T * a.n_heads * (D / 64);
+    auto launch_join = [&](auto kern, dim3 grid, int threads) { hipLaunchKernelGGL(kern, grid, dim3(threads), 0, st, a); };
+    if (chunks <= 128) launch_join(k_attn_join<D, 16 * MT, SH::STEP, 64, 16>, dim3(a.T, a.n_heads * (D / 64)), 16 * WAVE);
+    else if (chunks <= 1024) launch_join(k_attn_join<D, 16 * MT, SH::STEP, 64, 4>, dim3(a.T, a.n_heads * (D / 64)), 4 * WAVE);
+    else launch_join(k_attn_join<D, 16 * MT, SH::STEP, D, 1>, dim3(a.T, (a.n_heads + NW - 1) / NW), AT_THREADS);
     return hipGetLastError();
 }
 
