@@ -11,6 +11,7 @@
 #include "device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -22,11 +23,16 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_RELU = 4 };
 
+// z / (1 + e^-y) by the hardware's exp2 and reciprocal (about 1 unit each)
+MOE_DEV float gated(float z, float y) {
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * y));
+}
 MOE_DEV float activate(float z, int act) {
     switch (act) {
-        case ACT_SILU: return z / (1.0f + expf(-z));
+        case ACT_SILU: return gated(z, z);
         case ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-        case ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+        // 0.5 z (1 + tanh u) = z / (1 + e^-2u)
+        case ACT_GELU_TANH: return gated(z, 1.59576912160573071f * (z + 0.044715f * z * z * z));
         case ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
     }
     return z;
@@ -50,15 +56,16 @@ MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 // the MFMA's work is thrown away, which costs nothing (T <= 16 leaves the matrix
 // cores idle), and in return the loads need neither LDS nor narrow rows.
 // All of a block's loads go out at once.
-constexpr int ROWS_MAX_T = 16;
+// More than 16 rows: TT tiles of 16, each with its own second operands and results.
+constexpr int ROWS_MAX_T = 32;
 constexpr int RW = 8;                      // waves per block
 
-template <int RG, int KS, int OB>
+template <int RG, int KS, int TT, int OB>
 __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __restrict__ x, int x_stride,
                                                               const uint16_t* __restrict__ w, const float* __restrict__ bias,
                                                               int act, const void* residual, int T, int N, int K,
                                                               int rows_per_block, void* out) {
-    __shared__ float red[RW][RG][WAVE];
+    __shared__ float red[RW][RG][TT][WAVE];
     const int l = lane_id(), wv = uni(threadIdx.x / WAVE), r = l & 15, g = l >> 4;
     const int n0 = blockIdx.x * rows_per_block, rows = min(rows_per_block, N - n0);
     const int kc = K / 8;                  // 16-byte chunks of a row
@@ -66,19 +73,23 @@ __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __
     const rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(w + (int64_t)n0 * K), 0, rows * K * 2, 0x00027000);
     const rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, ((T - 1) * x_stride + K) * 2, 0x00027000);
     const int chunk = 4 * g + (r & 3);
-    float val[RG];
+    float val[RG][TT];
 #pragma unroll
-    for (int i = 0; i < RG; i++) val[i] = 0.f;
+    for (int i = 0; i < RG; i++)
+#pragma unroll
+        for (int t = 0; t < TT; t++) val[i][t] = 0.f;
     for (int s0 = wv * KS; s0 * 16 < kc; s0 += RW * KS) {
-        u32x4_l xf[KS][4], wf[RG][KS];
+        u32x4_l xf[TT][KS][4], wf[RG][KS];
 #pragma unroll
-        for (int s = 0; s < KS; s++)
+        for (int t = 0; t < TT; t++)
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                const int c = (s0 + s) * 16 + 4 * g + p;
-                xf[s][p] = __builtin_bit_cast(u32x4_l, __builtin_amdgcn_raw_buffer_load_b128(
-                                                           xr, c < kc && r < T ? (r * x_stride + c * 8) * 2 : -16, 0, 0));
-            }
+            for (int s = 0; s < KS; s++)
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    const int c = (s0 + s) * 16 + 4 * g + p, row = 16 * t + r;
+                    xf[t][s][p] = __builtin_bit_cast(u32x4_l, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                  xr, c < kc && row < T ? (row * x_stride + c * 8) * 2 : -16, 0, 0));
+                }
 #pragma unroll
         for (int i = 0; i < RG; i++)
 #pragma unroll
@@ -88,28 +99,32 @@ __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __
                                                            wr, c < kc && row < rows ? (row * K + c * 8) * 2 : -16, 0, 2));
             }
 #pragma unroll
-        for (int i = 0; i < RG; i++) {
-            f32x4_t acc[4];
+        for (int i = 0; i < RG; i++)
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < TT; t++) {
+                f32x4_t acc[4];
 #pragma unroll
-                for (int s = 0; s < KS; s++)
-                    acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wf[i][s]),
-                                                                     __builtin_bit_cast(bf16x8_t, xf[s][p]), acc[p], 0, 0, 0);
+                for (int p = 0; p < 4; p++) {
+                    acc[p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < KS; s++)
+                        acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wf[i][s]),
+                                                                         __builtin_bit_cast(bf16x8_t, xf[t][s][p]), acc[p], 0, 0, 0);
+                }
+                val[i][t] += (acc[0][0] + acc[1][1]) + (acc[2][2] + acc[3][3]);
             }
-            val[i] += (acc[0][0] + acc[1][1]) + (acc[2][2] + acc[3][3]);
-        }
     }
 #pragma unroll
-    for (int i = 0; i < RG; i++) red[wv][i][l] = val[i];
+    for (int i = 0; i < RG; i++)
+#pragma unroll
+        for (int t = 0; t < TT; t++) red[wv][i][t][l] = val[i][t];
     __syncthreads();
     // thread: output (t, row), the rows of a token side by side
     for (int id = threadIdx.x; id < T * rows; id += RW * WAVE) {
         const int t = id / rows, row = id - t * rows;
         float z = 0.f;
 #pragma unroll
-        for (int i = 0; i < RW; i++) z += red[i][row >> 2][(row & 3) * 16 + t];
+        for (int i = 0; i < RW; i++) z += red[i][row >> 2][t >> 4][(row & 3) * 16 + (t & 15)];
         const int n = n0 + row;
         if (bias) z += bias[n];
         z = activate(z, act);
@@ -199,6 +214,7 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
     const int nk = K / BK;
     auto issue = [&](int k) __attribute__((always_inline)) {
         unsigned char* st = smem + (k % ST) * G::STAGE;
+        k = min(k, nk - 1);
 #pragma unroll
         for (int i = 0; i < G::DX; i++) dma16(xb + (int64_t)k * G::ROWB + xo[i], (lds_ptr*)(st + (wv * G::DX + i) * 1024));
 #pragma unroll
@@ -241,40 +257,47 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.w[j][q], f.x[i][q], acc[i][j], 0, 0, 0);
     };
     // One K step: stage k + 1 has landed everywhere (each wave waits for its own
-    // loads, then the barrier); stage k - 1, read one step earlier still, is free
-    // for step k + ST - 1; the next fragments are read under this step's MFMAs.
+    // loads, then the barrier); the next fragments are read under this step's
+    // MFMAs; stage k - 1, read one step earlier still, is free and takes the loads
+    // of step k + ST - 1.  Every step is the same, with no branch that would make
+    // the MFMAs wait: behind the last one the last K block is loaded again and the
+    // fragments read go unused.
     auto step = [&](int k, Frag& cur, Frag& nxt) __attribute__((always_inline)) {
-        const int left = nk - 1 - k;                          // steps after this one
-        if (left >= ST - 2) wait_vm<G::DMA * (ST - 3)>();
-        else wait_vm<0>();
-        asm volatile("" ::: "memory");
+        wait_vm<G::DMA * (ST - 3)>();
         __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (left >= ST - 1) issue(k + ST - 1);
-        if (left >= 1) read(nxt, k + 1);
+        read(nxt, k + 1);
+        issue(k + ST - 1);
         mma(cur);
+        constexpr int NM = IT * JT * KQ, NR = (IT + JT) * KQ, H = NM / 2 < 8 ? NM / 2 : 8;
+#pragma unroll
+        for (int q = 0; q < H; q++) {
+            __builtin_amdgcn_sched_group_barrier(0x100, (NR + H - 1) / H, 0);        // LDS reads
+            __builtin_amdgcn_sched_group_barrier(0x008, NM / H / 2, 0);              // MFMA
+        }
+#pragma unroll
+        for (int q = 0; q < H; q++) {
+            __builtin_amdgcn_sched_group_barrier(0x020, (G::DMA + H - 1) / H, 0);    // LDS DMA
+            __builtin_amdgcn_sched_group_barrier(0x008, NM / H / 2, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
-    for (int s = 0; s < ST - 1; s++)
-        if (s < nk) issue(s);
+    for (int s = 0; s < ST - 1; s++) issue(s);
     Frag f0, f1;
-    if (nk >= ST - 1) wait_vm<G::DMA * (ST - 2)>();
-    else wait_vm<0>();
+    wait_vm<G::DMA * (ST - 2)>();
     __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
     read(f0, 0);
-    int k = 0;
-    for (; k + 1 < nk; k += 2) {
+    for (int k = 0; k + 1 < nk; k += 2) {
         step(k, f0, f1);
         step(k + 1, f1, f0);
     }
-    if (k < nk) mma(f0);
+    if constexpr (BK == 64)                 // (K is a multiple of 64: an even number of steps of 32)
+        if (nk & 1) step(nk - 1, f0, f1);
+    wait_vm<0>();
 
     // ---- epilogue: 32 rows of the wave's tile at a time through its part of the
     // LDS, then 8 consecutive outputs a lane
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();                             // every wave has read its last fragments
-    asm volatile("" ::: "memory");
+    __syncthreads();                                          // every wave has read its last fragments, every load has landed
     unsigned char* ep = smem + wv * 32 * G::EROW;
 #pragma unroll 1
     for (int i = 0; i < IT; i++) {
@@ -343,21 +366,27 @@ struct LinearArgs {
     void* out;
 };
 
-template <int RG, int KS, int OB>
+template <int RG, int KS, int TT, int OB>
 hipError_t launch_rows(const LinearArgs& a, int rows_per_block, hipStream_t st) {
-    hipLaunchKernelGGL((k_linear_rows<RG, KS, OB>), dim3((a.N + rows_per_block - 1) / rows_per_block), dim3(RW * WAVE), 0,
-                       st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual, a.T, a.N, a.K, rows_per_block, a.out);
+    hipLaunchKernelGGL((k_linear_rows<RG, KS, TT, OB>), dim3((a.N + rows_per_block - 1) / rows_per_block), dim3(RW * WAVE),
+                       0, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual, a.T, a.N, a.K, rows_per_block, a.out);
     return hipGetLastError();
 }
 
 template <int KS, int OB>
 hipError_t launch_rows_k(const LinearArgs& a, hipStream_t st) {
-    // one block per CU while it has at most 32 rows
-    const int groups = (a.N + 3) / 4, rg = std::min(std::max((groups + 255) / 256, 1), 8);
-    if (rg == 1) return launch_rows<1, KS, OB>(a, 4, st);
-    if (rg == 2) return launch_rows<2, KS, OB>(a, 8, st);
-    if (rg <= 4) return launch_rows<4, KS, OB>(a, 4 * rg, st);
-    return launch_rows<8, KS, OB>(a, 4 * rg, st);
+    // one block per CU while it has at most 32 weight rows (16 with more than 16 rows of x)
+    const int groups = (a.N + 3) / 4, rg = std::min(std::max((groups + 255) / 256, 1), a.T <= 16 ? 8 : 4);
+    if (a.T <= 16) {
+        if (rg == 1) return launch_rows<1, KS, 1, OB>(a, 4, st);
+        if (rg == 2) return launch_rows<2, KS, 1, OB>(a, 8, st);
+        if (rg <= 4) return launch_rows<4, KS, 1, OB>(a, 4 * rg, st);
+        return launch_rows<8, KS, 1, OB>(a, 4 * rg, st);
+    }
+    if constexpr (KS == 1) {
+        return rg <= 2 ? launch_rows<2, 1, 2, OB>(a, 4 * rg, st) : launch_rows<4, 1, 2, OB>(a, 4 * rg, st);
+    }
+    return hipErrorInvalidValue;
 }
 
 template <int BT, int BN, int BK, int ST, int BPC, int OB>
@@ -376,14 +405,14 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
 template <int OB>
 hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
     if (a.T <= ROWS_MAX_T) {
-        if (a.K <= 1024) return launch_rows_k<1, OB>(a, st);
+        if (a.K <= 1024 || a.T > 16) return launch_rows_k<1, OB>(a, st);
         if (a.K <= 2048) return launch_rows_k<2, OB>(a, st);
         return launch_rows_k<4, OB>(a, st);
     }
     auto tiles = [&](int bt, int bn) { return (int64_t)((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
     if (tiles(256, 256) >= 192) return launch_tile<256, 256, 32, 4, 1, OB>(a, st);
     if (tiles(128, 128) >= 192) return launch_tile<128, 128, 32, 4, 2, OB>(a, st);
-    return launch_tile<64, 64, 64, 4, 2, OB>(a, st);
+    return launch_tile<64, 64, 64, 8, 1, OB>(a, st);
 }
 
 }  // namespace
