@@ -142,48 +142,50 @@ __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __
 // ------------------------------------------------------------------ many rows
 // BT x BN output tiles, K steps of BK through ST LDS stages filled by the LDS DMA
 // (16 bytes a lane), ST - 1 steps ahead: a stage is waited for ST - 2 steps after
-// its loads went out.  Four waves in 2 x 2, MFMA 32x32x16 with the weight as the
-// first operand, so a lane's results are runs of 4 consecutive outputs of one
-// row.  The fragments of the next K step are read from LDS under the MFMAs of the
+// its loads went out.  2 x WN waves, MFMA 16x16x32 with the weight as the
+// first operand, so a lane's results are 4 consecutive outputs of one row.  The fragments of the next K step are read from LDS under the MFMAs of the
 // current one, in two register sets.
 //   LDS rows are BK elements; their 16-byte chunks are swizzled (on the global
-// side of the DMA) so that 8 rows' reads of one chunk fall into 8 different
-// bank groups: BK 64 (128-byte rows): chunk ^ (row & 7); BK 32 (two rows per
-// 128 bytes): chunk ^ ((row >> 1) & 3).
+// side of the DMA) so that the 16 lanes that a 16-byte read serves together fall
+// into the 16 slots of 256 bytes (lanes 0-3, 12-15 and 20-27 are served together,
+// 4-11, 16-19 and 28-31, and so on): BK 64, chunk ^ ((row >> 1) & 7); BK 32, chunk ^
+// {0, 2, 3, 1}[(row >> 2) & 3].  No conflicts counted.
 //   Blocks: tiles of one XCD (block mod 8) are neighbours, in panels of 8 column
 // tiles, so that they share x and w in its L2.
-constexpr int TILE_THREADS = 256;
-
+// s_waitcnt vmcnt(N) lgkmcnt(0): this wave's older loads have landed, its LDS reads
+// are done (they went out a step of MFMAs ago; said here, or the compiler would
+// wait for the next step's reads too)
 template <int N>
 MOE_DEV void wait_vm() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
 }
 MOE_DEV void dma16(const void* g, lds_ptr* l) { __builtin_amdgcn_global_load_lds(g, l, 16, 0, 0); }
 
-template <int BT, int BN, int BK, int ST>
+template <int BT, int BN, int BK, int ST, int WN>
 struct TileGeo {
-    static constexpr int WT = BT / 2, WNC = BN / 2;          // a wave's rows and columns
-    static constexpr int IT = WT / 32, JT = WNC / 32;        // its MFMA tiles
+    static constexpr int NWV = 2 * WN;                       // waves: 2 along the rows, WN along the columns
+    static constexpr int WT = BT / 2, WNC = BN / WN;         // a wave's rows and columns
+    static constexpr int IT = WT / 16, JT = WNC / 16;        // its MFMA tiles
     static constexpr int ROWB = BK * 2;                      // LDS row bytes
     static constexpr int STAGE = (BT + BN) * ROWB;
     static constexpr int RPI = 1024 / ROWB;                  // rows per DMA instruction (1 KB)
-    static constexpr int DX = BT / RPI / 4, DW = BN / RPI / 4, DMA = DX + DW;   // per wave
-    static_assert(DX * RPI * 4 == BT && DW * RPI * 4 == BN, "whole DMA instructions per wave");
+    static constexpr int DX = BT / RPI / NWV, DW = BN / RPI / NWV, DMA = DX + DW;   // per wave
+    static_assert(DX * RPI * NWV == BT && DW * RPI * NWV == BN, "whole DMA instructions per wave");
     // epilogue: 32 rows x WNC columns fp32 per wave, rows padded by 16 bytes
-    static constexpr int EROW = WNC * 4 + 16, EPI = 4 * 32 * EROW;
+    static constexpr int EROW = WNC * 4 + 16, EPI = NWV * 32 * EROW;
     static constexpr int LDS = STAGE * ST > EPI ? STAGE * ST : EPI;
 };
 
-template <int BT, int BN, int BK, int ST, int OB, int BPC>
-__global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_t* __restrict__ x, int x_stride,
+template <int BT, int BN, int BK, int ST, int WN, int OB, int BPC>
+__global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(const uint16_t* __restrict__ x, int x_stride,
                                                                    const uint16_t* __restrict__ w,
                                                                    const float* __restrict__ bias, int act,
                                                                    const void* residual, int T, int N, int K, int tiles_t,
                                                                    int tiles_n, void* out) {
-    using G = TileGeo<BT, BN, BK, ST>;
-    constexpr int IT = G::IT, JT = G::JT, KQ = BK / 16;      // MFMA steps per K step
+    using G = TileGeo<BT, BN, BK, ST, WN>;
+    constexpr int IT = G::IT, JT = G::JT, KQ = BK / 32;      // MFMA steps per K step
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), wt = wv >> 1, wn = wv & 1;
+    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), wt = wv / WN, wn = wv % WN;
     // tile of this block
     const int tiles = tiles_t * tiles_n, per = (tiles + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -197,7 +199,9 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
     // DMA: lane -> row l / CPR of the instruction's rows, LDS chunk l % CPR, which
     // holds global chunk (l % CPR) ^ swizzle(row).  Rows past the end repeat the last.
     constexpr int CPR = G::ROWB / 16;
-    auto swz = [](int row) __attribute__((always_inline)) { return BK == 64 ? row & 7 : (row >> 1) & 3; };
+    auto swz = [](int row) __attribute__((always_inline)) {
+        return BK == 64 ? (row >> 1) & 7 : (((row >> 2) ^ (row >> 3)) & 1) * 2 + ((row >> 3) & 1);
+    };
     const unsigned char* xb = (const unsigned char*)(x + t0 * x_stride);
     const unsigned char* wb = (const unsigned char*)(w + (int64_t)n0 * K);
     uint32_t xo[G::DX], wo[G::DW];
@@ -221,32 +225,30 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
         for (int i = 0; i < G::DW; i++)
             dma16(wb + (int64_t)k * G::ROWB + wo[i], (lds_ptr*)(st + BT * G::ROWB + (wv * G::DW + i) * 1024));
     };
-    const int fr = l & 31, fh = l >> 5;
+    const int fr = l & 15, fh = l >> 4;
     struct Frag { bf16x8_t x[IT][KQ], w[JT][KQ]; };
     auto read = [&](Frag& f, int k) __attribute__((always_inline)) {
         const unsigned char* st = smem + (k % ST) * G::STAGE;
 #pragma unroll
         for (int q = 0; q < KQ; q++) {
-            const int c = q * 2 + fh;
+            const int c = q * 4 + fh;
 #pragma unroll
             for (int i = 0; i < IT; i++) {
-                const int r = wt * G::WT + i * 32 + fr;
+                const int r = wt * G::WT + i * 16 + fr;
                 f.x[i][q] = *reinterpret_cast<const bf16x8_t*>(st + r * G::ROWB + ((c ^ swz(r)) * 16));
             }
 #pragma unroll
             for (int j = 0; j < JT; j++) {
-                const int r = wn * G::WNC + j * 32 + fr;
+                const int r = wn * G::WNC + j * 16 + fr;
                 f.w[j][q] = *reinterpret_cast<const bf16x8_t*>(st + BT * G::ROWB + r * G::ROWB + ((c ^ swz(r)) * 16));
             }
         }
     };
-    f32x16_t acc[IT][JT];
+    f32x4_t acc[IT][JT];
 #pragma unroll
     for (int i = 0; i < IT; i++)
 #pragma unroll
-        for (int j = 0; j < JT; j++)
-#pragma unroll
-            for (int v = 0; v < 16; v++) acc[i][j][v] = 0.f;
+        for (int j = 0; j < JT; j++) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     auto mma = [&](const Frag& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < KQ; q++)
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
             for (int i = 0; i < IT; i++)
 #pragma unroll
                 for (int j = 0; j < JT; j++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.w[j][q], f.x[i][q], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[j][q], f.x[i][q], acc[i][j], 0, 0, 0);
     };
     // One K step: stage k + 1 has landed everywhere (each wave waits for its own
     // loads, then the barrier); the next fragments are read under this step's
@@ -268,7 +270,7 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
         read(nxt, k + 1);
         issue(k + ST - 1);
         mma(cur);
-        constexpr int NM = IT * JT * KQ, NR = (IT + JT) * KQ, H = NM / 2 < 8 ? NM / 2 : 8;
+        constexpr int NM = IT * JT * KQ, NR = (IT + JT) * KQ, H = NM / 2 < 16 ? NM / 2 : 16;
 #pragma unroll
         for (int q = 0; q < H; q++) {
             __builtin_amdgcn_sched_group_barrier(0x100, (NR + H - 1) / H, 0);        // LDS reads
@@ -299,59 +301,83 @@ __global__ __launch_bounds__(TILE_THREADS, BPC) void k_linear_tile(const uint16_
     // LDS, then 8 consecutive outputs a lane
     __syncthreads();                                          // every wave has read its last fragments, every load has landed
     unsigned char* ep = smem + wv * 32 * G::EROW;
-#pragma unroll 1
-    for (int i = 0; i < IT; i++) {
-#pragma unroll
-        for (int q = 0; q < IT; q++) {
-            if (i != q) continue;                             // uniform
-#pragma unroll
-            for (int j = 0; j < JT; j++)
-#pragma unroll
-                for (int v = 0; v < 4; v++)
-                    *reinterpret_cast<f32x4_t*>(ep + fr * G::EROW + (j * 32 + v * 8 + fh * 4) * 4) =
-                        f32x4_t{acc[q][j][4 * v], acc[q][j][4 * v + 1], acc[q][j][4 * v + 2], acc[q][j][4 * v + 3]};
-        }
+    constexpr int LPR = G::WNC / 8, RPP = WAVE / LPR, NP = 32 / RPP;     // lanes per row, rows per pass, passes
+    const int er = l / LPR, ec = l % LPR * 8, n = n0 + wn * G::WNC + ec;
+    f32x4_t b[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (bias && n < N) {
+        b[0] = *reinterpret_cast<const f32x4_t*>(bias + n);
+        b[1] = *reinterpret_cast<const f32x4_t*>(bias + n + 4);
+    }
+    auto fence = [&]() __attribute__((always_inline)) {
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
         __builtin_amdgcn_wave_barrier();
-        constexpr int LPR = G::WNC / 8, RPP = WAVE / LPR;     // lanes per row, rows per pass
+    };
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += RPP) {
-            const int r = r0 + l / LPR, c = l % LPR * 8;
-            const int64_t t = t0 + wt * G::WT + i * 32 + r;
-            const int n = n0 + wn * G::WNC + c;
-            f32x4_t z[2];
-            z[0] = *reinterpret_cast<const f32x4_t*>(ep + r * G::EROW + c * 4);
-            z[1] = *reinterpret_cast<const f32x4_t*>(ep + r * G::EROW + c * 4 + 16);
-            if (t >= T || n >= N) continue;
-            if (bias) {
-                z[0] += *reinterpret_cast<const f32x4_t*>(bias + n);
-                z[1] += *reinterpret_cast<const f32x4_t*>(bias + n + 4);
-            }
-            if (act != ACT_NONE)
-#pragma unroll 1
-                for (int h = 0; h < 2; h++)
+    for (int i = 0; i < IT / 2; i++) {
+        // all of the block's residual goes out first
+        const int64_t tw = t0 + wt * G::WT + i * 32 + er, ow = tw * N + n;
+        u32x4_l rv[NP][OB ? 1 : 2];
+        if (residual) {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) z[h][e] = activate(z[h][e], act);
-            const int64_t o = t * N + n;
+            for (int q = 0; q < NP; q++) {
+                if (tw + q * RPP < T && n < N) {
+                    const int64_t o = ow + (int64_t)q * RPP * N;
+                    if constexpr (OB) {
+                        rv[q][0] = *reinterpret_cast<const u32x4_l*>((const uint16_t*)residual + o);
+                    } else {
+                        rv[q][0] = *reinterpret_cast<const u32x4_l*>((const float*)residual + o);
+                        rv[q][OB ? 0 : 1] = *reinterpret_cast<const u32x4_l*>((const float*)residual + o + 4);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < IT; q++) {
+            if (i != q / 2) continue;                         // uniform
+#pragma unroll
+            for (int j = 0; j < JT; j++)
+                *reinterpret_cast<f32x4_t*>(ep + (q % 2 * 16 + fr) * G::EROW + (j * 16 + fh * 4) * 4) = acc[q][j];
+        }
+        fence();
+        if (act != ACT_NONE) {                                // in place, a loop of its own
+#pragma unroll 1
+            for (int q = 0; q < 2 * NP; q++) {
+                f32x4_t* z = reinterpret_cast<f32x4_t*>(ep + (q / 2 * RPP + er) * G::EROW + ec * 4 + (q & 1) * 16);
+                f32x4_t y = *z + (q & 1 ? b[1] : b[0]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) y[e] = activate(y[e], act);
+                *z = y;
+            }
+            fence();
+        }
+#pragma unroll
+        for (int q = 0; q < NP; q++) {
+            const float* src = reinterpret_cast<const float*>(ep + (q * RPP + er) * G::EROW + ec * 4);
+            f32x4_t z[2] = {*reinterpret_cast<const f32x4_t*>(src), *reinterpret_cast<const f32x4_t*>(src + 4)};
+            if (tw + q * RPP >= T || n >= N) continue;
+            if (act == ACT_NONE) {
+                z[0] += b[0];
+                z[1] += b[1];
+            }
+            const int64_t o = ow + (int64_t)q * RPP * N;
             if constexpr (OB) {
                 if (residual) {
-                    const u32x4_l q = *reinterpret_cast<const u32x4_l*>((const uint16_t*)residual + o);
-                    z[0] += f32x4_t{bf16lo_to_f32(q[0]), bf16hi_to_f32(q[0]), bf16lo_to_f32(q[1]), bf16hi_to_f32(q[1])};
-                    z[1] += f32x4_t{bf16lo_to_f32(q[2]), bf16hi_to_f32(q[2]), bf16lo_to_f32(q[3]), bf16hi_to_f32(q[3])};
+                    const u32x4_l r = rv[q][0];
+                    z[0] += f32x4_t{bf16lo_to_f32(r[0]), bf16hi_to_f32(r[0]), bf16lo_to_f32(r[1]), bf16hi_to_f32(r[1])};
+                    z[1] += f32x4_t{bf16lo_to_f32(r[2]), bf16hi_to_f32(r[2]), bf16lo_to_f32(r[3]), bf16hi_to_f32(r[3])};
                 }
                 *reinterpret_cast<u32x4_l*>((uint16_t*)out + o) =
                     u32x4_l{pk(z[0][0], z[0][1]), pk(z[0][2], z[0][3]), pk(z[1][0], z[1][1]), pk(z[1][2], z[1][3])};
             } else {
                 if (residual) {
-                    z[0] += *reinterpret_cast<const f32x4_t*>((const float*)residual + o);
-                    z[1] += *reinterpret_cast<const f32x4_t*>((const float*)residual + o + 4);
+                    z[0] += __builtin_bit_cast(f32x4_t, rv[q][0]);
+                    z[1] += __builtin_bit_cast(f32x4_t, rv[q][OB ? 0 : 1]);
                 }
                 *reinterpret_cast<f32x4_t*>((float*)out + o) = z[0];
                 *reinterpret_cast<f32x4_t*>((float*)out + o + 4) = z[1];
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-        __builtin_amdgcn_wave_barrier();
+        fence();
     }
 }
 
@@ -389,15 +415,15 @@ hipError_t launch_rows_k(const LinearArgs& a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-template <int BT, int BN, int BK, int ST, int BPC, int OB>
+template <int BT, int BN, int BK, int ST, int WN, int BPC, int OB>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
-    auto kern = k_linear_tile<BT, BN, BK, ST, OB, BPC>;
+    auto kern = k_linear_tile<BT, BN, BK, ST, WN, OB, BPC>;
     static LdsLimit lim;
-    constexpr int lds = TileGeo<BT, BN, BK, ST>::LDS;
+    constexpr int lds = TileGeo<BT, BN, BK, ST, WN>::LDS;
     hipError_t e = lim.ensure((const void*)kern, lds);
     if (e != hipSuccess) return e;
     const int tt = (a.T + BT - 1) / BT, tn = (a.N + BN - 1) / BN, per = (tt * tn + 7) / 8;
-    hipLaunchKernelGGL(kern, dim3(per * 8), dim3(TILE_THREADS), lds, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual,
+    hipLaunchKernelGGL(kern, dim3(per * 8), dim3(2 * WN * WAVE), lds, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual,
                        a.T, a.N, a.K, tt, tn, a.out);
     return hipGetLastError();
 }
@@ -410,9 +436,9 @@ hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
         return launch_rows_k<4, OB>(a, st);
     }
     auto tiles = [&](int bt, int bn) { return (int64_t)((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= 192) return launch_tile<256, 256, 32, 4, 1, OB>(a, st);
-    if (tiles(128, 128) >= 192) return launch_tile<128, 128, 32, 4, 2, OB>(a, st);
-    return launch_tile<64, 64, 64, 8, 1, OB>(a, st);
+    if (tiles(256, 256) >= 192) return launch_tile<256, 256, 32, 4, 4, 1, OB>(a, st);
+    if (tiles(128, 128) >= 192) return launch_tile<128, 128, 32, 4, 2, 2, OB>(a, st);
+    return launch_tile<64, 64, 64, 8, 2, 1, OB>(a, st);
 }
 
 }  // namespace
