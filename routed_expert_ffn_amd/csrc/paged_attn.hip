@@ -363,7 +363,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             return a.q + (int64_t)(rq.row0 + i0 + i) * a.q_stride + (int64_t)(head * G + g) * D;
         };
         // the loads go out before the first tile's: they are waited for first
-        constexpr int QN = QREG ? 1 : RB * (D / 8) / AT_THREADS;
+        constexpr int QC = RB * (D / 8), QN = QREG ? 1 : (QC + AT_THREADS - 1) / AT_THREADS;
         bf16x8_t qf[QREG ? MT : 1][QREG ? D / 32 : 1];
         u32x4_a qv[QN];
         if constexpr (QREG) {
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         } else {
 #pragma unroll
             for (int n = 0; n < QN; n++) {
-                const int c = n * AT_THREADS + tid;
+                const int c = min(n * AT_THREADS + tid, QC - 1);
                 qv[n] = *reinterpret_cast<const u32x4_a*>(q_row(c / (D / 8)) + c % (D / 8) * 8);
             }
         }
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         if constexpr (!QREG) {
 #pragma unroll
             for (int n = 0; n < QN; n++) {
-                const int c = n * AT_THREADS + tid;
+                const int c = min(n * AT_THREADS + tid, QC - 1);        // (the last chunk again, the same value)
                 *reinterpret_cast<u32x4_a*>(qs + c / (D / 8) * QP + c % (D / 8) * 8) = qv[n];
             }
         }

@@ -529,18 +529,16 @@ _FP8 = torch.float8_e4m3fn
 def _elsewhere(dev: int, stream) -> bool:
     """Whether a call has to switch to its tensors' device or to the given stream first (outputs and
     workspaces it allocates then belong to that stream)."""
-    return stream is not None or (dev >= 0 and dev != torch.cuda.current_device())
+    return stream is not None or (dev >= 0 and dev != torch._C._cuda_getDevice())
 
 
-def _current(dev: int) -> int:
-    """The current stream of a device, as the library takes it."""
-    return torch._C._cuda_getCurrentRawStream(dev)
+# the current stream of a device, as the library takes it
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(dev: int, t, name, dtype=None, shape=None):
+def _on(dev: int, t, name, dtype, shape):
     """t's address, after the checks (one pass over them where all hold)."""
-    if t.get_device() == dev and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape) \
-            and t.is_contiguous() and dev >= 0:
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous() and dev >= 0:
         return t.data_ptr()
     _need(t, name, dtype, shape)
     raise ValueError(f"{name} is on {t.device}, expected device {dev}")
@@ -550,8 +548,19 @@ def _opt(dev: int, t, name, dtype, shape):
     return None if t is None else _on(dev, t, name, dtype, shape)
 
 
+def _bytes(dev: int, nbytes: int, ws):
+    """A workspace of nbytes on the device: the given one where it is large enough, else a new one."""
+    if ws is None or ws.numel() * ws.element_size() < nbytes:
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on device {dev}")
+    return ws
+
+
 def _rows(t, name, dtype):
     """A [T][n] tensor whose rows are contiguous (they may lie apart)."""
+    if t.dim() == 2 and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t.shape[1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != dtype:
@@ -628,11 +637,13 @@ def kv_plan(cached_len, new_len, free_pages, page_table, page_size: int, T: int,
             return kv_plan(cached_len, new_len, free_pages, page_table, page_size, T, out=out)
     S, W = page_table.shape
     a, b = _on(dev, cached_len, "cached_len", i32, (S,)), _on(dev, new_len, "new_len", i32, (S,))
-    f, t = _on(dev, free_pages, "free_pages", i32), _on(dev, page_table, "page_table", i32)
+    n = free_pages.numel()
+    f, t = _on(dev, free_pages, "free_pages", i32, (n,)), _on(dev, page_table, "page_table", i32, (S, W))
     p = out if out is not None else KVPlan.allocate(S, T, cached_len.device)
     if (p.S, p.T, p.device) != (S, T, dev):
         raise ValueError(f"out holds {p.S} requests and {p.T} rows on device {p.device}, expected {S}, {T} on {dev}")
-    _chk(load().moe_kv_plan(a, b, S, f, free_pages.numel(), page_size, T, t, W, *p.ptrs, _current(dev)), "moe_kv_plan")
+    rc = load().moe_kv_plan(a, b, S, f, n, page_size, T, t, W, *p.ptrs, _current(dev))
+    _chk(rc, "moe_kv_plan")
     return p
 
 
@@ -655,11 +666,11 @@ def qk_norm_rope(qkv, cache: KVCache, positions, slots, q_weight=None, k_weight=
         raise ValueError(f"qkv rows of {n} elements are not (n_heads + 2 * {cache.n_kv_heads}) heads of {D}")
     if cache.device != dev:
         raise ValueError(f"the cache is on device {cache.device}, expected {dev}")
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
     q = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=qkv.device)
     _chk(load().moe_qk_norm_rope(qkv.data_ptr(), BF16, stride, T, Hq, cache.ref,
                                  _opt(dev, q_weight, "q_weight", f32, (D,)), _opt(dev, k_weight, "k_weight", f32, (D,)),
-                                 eps, _opt(dev, inv_freq, "inv_freq", f32, None),
-                                 0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, rope_scale,
+                                 eps, _opt(dev, inv_freq, "inv_freq", f32, (R // 2,)), R, 1 if interleaved else 0, rope_scale,
                                  _on(dev, positions, "positions", i32, (T,)), _on(dev, slots, "slots", i32, (T,)),
                                  _on(dev, q, "out", torch.bfloat16, (T, Hq, D)), _current(dev)), "moe_qk_norm_rope")
     return q
@@ -695,11 +706,11 @@ def paged_attention(q, cache: KVCache, page_table, q_offsets, kv_len, scale=None
     S, W = page_table.shape
     o = out if out is not None else torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     nb = paged_attention_workspace_size(T, Hq, cache.n_kv_heads, D, S)
-    ws = _workspace(nb, q.device, workspace)
-    _chk(load().moe_paged_attn(q.data_ptr(), BF16, stride, T, Hq, cache.ref, _on(dev, page_table, "page_table", i32), W,
+    ws = _bytes(dev, nb, workspace)
+    _chk(load().moe_paged_attn(q.data_ptr(), BF16, stride, T, Hq, cache.ref, _on(dev, page_table, "page_table", i32, (S, W)), W,
                                _on(dev, q_offsets, "q_offsets", i32, (S + 1,)), _on(dev, kv_len, "kv_len", i32, (S,)), S,
                                D ** -0.5 if scale is None else scale, softcap, window,
-                               _on(dev, o, "out", torch.bfloat16, (T, Hq, D)), _on(dev, ws, "workspace"), nb,
+                               _on(dev, o, "out", torch.bfloat16, (T, Hq, D)), ws.data_ptr(), nb,
                                _current(dev)), "moe_paged_attn")
     return o
 
@@ -728,9 +739,48 @@ def linear(x, w, bias=None, act=None, residual=None, out_dtype=None, out=None, w
         out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
     o = out if out is not None else torch.empty((T, N), dtype=out_dtype, device=x.device)
     nb = linear_workspace_size(T, N, K)
-    ws = _on(dev, _workspace(nb, x.device, workspace), "workspace") if nb else None
+    ws = _bytes(dev, nb, workspace).data_ptr() if nb else None
     _chk(load().moe_linear(x.data_ptr(), BF16, stride, _on(dev, w, "w", torch.bfloat16, (N, K)), BF16,
                            _opt(dev, bias, "bias", torch.float32, (N,)), _ACT[act],
                            _opt(dev, residual, "residual", out_dtype, (T, N)), T, N, K,
                            _on(dev, o, "out", out_dtype, (T, N)), _act_dtype(o), ws, nb, _current(dev)), "moe_linear")
     return o
+
+
+class AttentionWorkspace:
+    """Preallocated buffers for repeated calls of `attention_layer` at one shape (T rows of H elements, S requests)."""
+
+    def __init__(self, T, H, n_heads, cache: KVCache, S, device="cuda"):
+        bf, D, Hkv = torch.bfloat16, cache.head_dim, cache.n_kv_heads
+        n = (n_heads + 2 * Hkv) * D
+        self.qkv = torch.empty((T, n), dtype=bf, device=device)
+        self.q = torch.empty((T, n_heads, D), dtype=bf, device=device)
+        self.o = torch.empty((T, n_heads, D), dtype=bf, device=device)
+        self.out = torch.empty((T, H), dtype=bf, device=device)
+        self.attn_ws = torch.empty(paged_attention_workspace_size(T, n_heads, Hkv, D, S), dtype=torch.uint8,
+                                   device=device)
+        self.linear_ws = torch.empty(max(linear_workspace_size(T, n, H), linear_workspace_size(T, H, n_heads * D), 1),
+                                     dtype=torch.uint8, device=device)
+
+
+def attention_layer(x, w_qkv, w_out, cache: KVCache, plan: KVPlan, page_table, q_weight=None, k_weight=None, eps=1e-6,
+                    inv_freq=None, interleaved=False, rope_scale=1.0, b_qkv=None, b_out=None, scale=None, softcap=0.0,
+                    window=0, residual=None, ws=None, stream=None, out=None):
+    """The attention half of a layer on the rows x [T][H] of one step (plan: kv_plan's outputs): the fused projection
+    w_qkv [(n_heads + 2 n_kv_heads) * head_dim][H], head norms + rotation + cache write, attention over the paged
+    cache and the output projection w_out [H][n_heads * head_dim], added to residual [T][H] (out may be it).  Rows
+    behind the step's last come out undefined.  `layer` is the other half."""
+    if _elsewhere(x.get_device(), stream):
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            return attention_layer(x, w_qkv, w_out, cache, plan, page_table, q_weight, k_weight, eps, inv_freq,
+                                   interleaved, rope_scale, b_qkv, b_out, scale, softcap, window, residual, ws, out=out)
+    if ws is None:
+        n_heads = w_qkv.shape[0] // cache.head_dim - 2 * cache.n_kv_heads
+        ws = AttentionWorkspace(x.shape[0], w_out.shape[0], n_heads, cache, page_table.shape[0], device=x.device)
+    linear(x, w_qkv, bias=b_qkv, out=ws.qkv, workspace=ws.linear_ws)
+    qk_norm_rope(ws.qkv, cache, plan.positions, plan.slots, q_weight, k_weight, eps, inv_freq, interleaved, rope_scale,
+                 out=ws.q)
+    paged_attention(ws.q, cache, page_table, plan.q_offsets, plan.kv_len, scale, softcap, window, out=ws.o,
+                    workspace=ws.attn_ws)
+    return linear(ws.o.view(ws.o.shape[0], -1), w_out, bias=b_out, residual=residual, out=ws.out if out is None else out,
+                  workspace=ws.linear_ws)

@@ -89,11 +89,12 @@ def attention(q, k, v, table, offs, lens, page, scale, softcap, window):
 def attention_bound(out, mass, reach, D, positions):
     """How far a bf16 result may be.  Scores: fp32 sums of D products (each of the D - 1 additions and the scaling off
     by 2^-24 relative to sum |q||k|), so a probability is off by that much relatively, once in itself and once in
-    the sum, plus 2^-20 for exp2 and the log2 e scaling of exponents up to 2^4; probabilities are rounded to bf16
-    (half a step, relative to sum p |v|); the second product sums `positions` terms in fp32; the result is rounded
-    to bf16 (half a step)."""
+    the sum, plus 2^-20 for exp2 and the log2 e scaling of exponents up to 2^4; the weights w_j = p_j (1 + e_j) of both
+    the product and the normalising sum are rounded to bf16, |e_j| <= half a step: sum w v / sum w - out =
+    sum p_j e_j (v_j - out) / sum w, at most half a step of (sum p |v| / sum p + |out|); the second product sums
+    `positions` terms in fp32; the result is rounded to bf16 (half a step)."""
     score = 2 * (D + 2) * F32_HALF * reach[..., None] + 2.0 ** -20
-    return (BF16_HALF + score + 2 * positions * F32_HALF) * mass + BF16_HALF * out.abs()
+    return (BF16_HALF + score + 2 * positions * F32_HALF) * (mass + out.abs()) + BF16_HALF * out.abs()
 
 
 def qk_norm_rope(qkv, Hq, Hkv, D, positions, qw, kw, eps, inv_freq, interleaved, rope_scale):

@@ -231,6 +231,13 @@ ATTNS = [
     ([5000], [1], 4, 1, 64, 16, False, 0, 0.0),                      # many splits
     ([3000, 10], [7, 7], 2, 1, 128, 32, True, 0, 0.0),
     ([5], [1], 64, 1, 64, 16, False, 0, 0.0),                        # the largest group
+    ([130, 100], [16, 16], 32, 2, 256, 32, False, 0, 0.0),           # all row tiles at head_dim 256
+    ([600, 33], [2, 3], 16, 1, 256, 16, True, 0, 25.0),
+    ([300, 64], [3, 1], 12, 1, 128, 16, True, 40, 0.0),
+    ([30, 17], [30, 17], 4, 2, 64, 16, False, 0, 0.0),               # whole prompts, three row tiles at head_dim 64
+    ([48, 50, 3], [48, 50, 3], 2, 2, 128, 16, True, 0, 0.0),
+    ([(i * 37) % 150 + 1 for i in range(70)], [1] * 70, 2, 1, 64, 16, False, 0, 0.0),     # more than 64 requests
+    ([(i * 53) % 90 + 4 for i in range(300)], [i % 4 for i in range(300)], 2, 2, 64, 16, True, 30, 0.0),
 ]
 
 
@@ -239,6 +246,15 @@ def test_paged_attention(case):
     lens, new, Hq, Hkv, D, page, fp8, window, cap = case
     st = attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=sum(lens), pad=2)
     check_attn(st, run_attn(st, softcap=cap, window=window), softcap=cap, window=window)
+
+
+@pytest.mark.parametrize("new", [1, 5, 10, 16, 23])                  # 4 rows each: one to four row tiles, and two units
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_paged_attention_every_shape(D, fp8, new):
+    st = attn_state([new + 150, new, new + 7], [new] * 3, 8, 2, D, 32, fp8, seed=new, pad=1)
+    check_attn(st, run_attn(st))
+    check_attn(st, run_attn(st, softcap=5.0, window=37), softcap=5.0, window=37)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -331,6 +347,13 @@ LINEARS = [
     (300, 1032, 128, "gelu", True, False, BF),
     (513, 768, 1024, None, False, True, torch.float32),
     (1100, 520, 192, "silu", True, True, BF),
+    (3, 40, 4160, None, True, True, BF),             # K past one round of the waves
+    (16, 264, 8256, "silu", False, True, torch.float32),
+    (2, 20000, 64, None, False, False, BF),          # more weight rows than blocks hold at once
+    (32, 4100 * 8, 64, "relu", True, False, BF),
+    (1700, 1800, 320, "gelu", True, True, BF),       # 128-square tiles
+    (3900, 3400, 192, None, False, True, BF),        # 256-square tiles
+    (3841, 3336, 64, "gelu_tanh", True, False, torch.float32),
 ]
 
 
@@ -373,3 +396,177 @@ def test_linear_infinities_stay_in_their_row_and_column():
     want = torch.ones(T, N, dtype=torch.bool)
     want[3], want[:, 7] = False, False
     assert torch.equal(fine, want)
+
+
+# ---------------------------------------------------------------- far addresses, streams, graphs, all of it together
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(fp8):
+    # a cache of over 2^31 elements (2^32 bytes): its last pages are written and read
+    D, Hkv, page, pages = 256, 2, 1024, 8300 if fp8 else 4200
+    cache = moe.KVCache.allocate(pages, page, Hkv, D, FP8 if fp8 else BF)
+    assert cache.k.numel() > 1 << 31
+    T, Hq, first = 70, 4, pages - 2
+    g = rng(11)
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g).to(BF)
+    table = ints([first, 0]).view(1, 2)                            # positions 0 .. 1023; the next page is the last one
+    plan = moe.kv_plan(ints([990]), ints([T]), ints([pages - 1]), table, page, T)
+    moe.qk_norm_rope(qkv.cuda(), cache, plan.positions, plan.slots)                 # earlier positions stay unwritten
+    q = qkv[:, :Hq * D].view(T, Hq, D)
+    got = moe.paged_attention(q.cuda(), cache, table, plan.q_offsets, plan.kv_len, window=1)    # each row sees itself
+    torch.cuda.synchronize()
+    v = qkv.view(T, Hq + 2 * Hkv, D)[:, Hq + Hkv:].double().repeat_interleave(Hq // Hkv, 1)
+    half = ref.FP8_HALF if fp8 else 0.0
+    bound = (half + 2 * ref.BF16_HALF) * v.abs() + (2.0 ** -10 / 448 * v.abs().amax(-1, keepdim=True) if fp8 else 0)
+    assert bool(((got.cpu().double() - v).abs() <= bound).all())
+
+
+def test_two_streams_at_once():
+    states = [attn_state([3000, 5], [1, 3], 8, 2, 128, 16, False, seed=s) for s in (20, 21)]
+    x = torch.randn(64, 1024).to(BF).cuda()
+    w = [torch.randn(512, 1024).to(BF).cuda() for _ in range(2)]
+    alone = [run_attn(st) for st in states]
+    lin = [moe.linear(x, v) for v in w]
+    args = [(st["q"].cuda(), st["cache"], st["table"].cuda(), ints(st["offs"]), ints(st["lens"])) for st in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [(moe.paged_attention(*a, stream=s), moe.linear(x, v, stream=s)) for a, v, s in zip(args, w, streams)]
+        torch.cuda.synchronize()
+        for (o, y), a, b, st in zip(got, alone, lin, states):
+            n = st["rows"]
+            assert torch.equal(o.cpu()[:n].view(torch.int16), a[:n].view(torch.int16))
+            assert torch.equal(y.view(torch.int16), b.view(torch.int16))
+
+
+class Model:
+    """Two requests through the attention half and the MoE half of one small layer."""
+
+    def __init__(self, fp8, T):
+        g = rng(31)
+        self.H, self.Hq, self.Hkv, self.D, self.page, self.S, self.T = 256, 4, 2, 64, 16, 2, T
+        r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        n = (self.Hq + 2 * self.Hkv) * self.D
+        self.w_qkv = (r(n, self.H) / 16).to(BF).cuda()
+        self.w_out = (r(self.H, self.Hq * self.D) / 16).to(BF).cuda()
+        self.qw, self.kw = (1 + 0.1 * r(self.D)).cuda(), (1 + 0.1 * r(self.D)).cuda()
+        self.freq = (10000.0 ** (-torch.arange(0, 32, 2) / 32)).float().cuda()
+        self.wr = (r(16, self.H) / 16).cuda()
+        self.wg, self.wu, self.wd = ((r(16, *s) / 16).to(BF).cuda() for s in ((128, self.H), (128, self.H), (self.H, 128)))
+        self.cache = moe.KVCache.allocate(40, self.page, self.Hkv, self.D, FP8 if fp8 else BF)
+        for t in (self.cache.k, self.cache.v):
+            t.view(torch.uint8).fill_(0x7F)                        # NaN wherever nothing was written
+        self.table = torch.full((2, 12), -1, dtype=torch.int32, device="cuda")
+        self.free = torch.randperm(40, generator=g).to(torch.int32).cuda()
+        self.cached, self.new = ints([0, 0]), ints([0, 0])
+        self.x = torch.zeros(T, self.H, dtype=BF, device="cuda")
+        self.plan = moe.KVPlan.allocate(2, T)
+        self.ws = moe.AttentionWorkspace(T, self.H, self.Hq, self.cache, 2)
+        self.lw = moe.LayerWorkspace(T, self.H, 16, 4, 128)
+        self.y = torch.empty_like(self.x)
+
+    def step(self):
+        moe.kv_plan(self.cached, self.new, self.free, self.table, self.page, self.T, out=self.plan)
+        h = moe.attention_layer(self.x, self.w_qkv, self.w_out, self.cache, self.plan, self.table, self.qw, self.kw,
+                                inv_freq=self.freq, residual=self.x, ws=self.ws)
+        moe.layer(h, self.wr, self.wg, self.wu, self.wd, 4, residual=h, lw=self.lw, out=self.y)
+
+    def advance(self):
+        """After a step: the new tokens are cached, and the pages that they took leave the list."""
+        taken = int(self.plan.counts[1])
+        self.cached += self.new
+        self.free.copy_(torch.roll(self.free, -taken))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_layer_steps_match_the_formulas(fp8):
+    # a ragged prompt chunk, a verify step, single tokens: each operator's output from its own inputs
+    m = Model(fp8, 48)
+    g = rng(32)
+    for new in ([30, 17], [5, 0], [1, 5], [1, 1]):
+        rows = sum(new)
+        m.new.copy_(ints(new))
+        m.x.copy_(torch.randn(m.T, m.H, generator=g).to(BF))
+        m.step()
+        torch.cuda.synchronize()
+        cached = m.cached.cpu().numpy()
+        want, size, y = ref.linear(m.x.cpu(), m.w_qkv.cpu(), None, None, None)
+        qkv = m.ws.qkv.cpu()
+        assert bool(((qkv.double() - want).abs() <= ref.linear_bound(want, size, y, m.H, BF)).all())
+        pos = m.plan.positions.cpu()
+        assert pos[:rows].tolist() == [c + i for c, n in zip(cached, new) for i in range(n)]
+        want, size = ref.qk_norm_rope(qkv, m.Hq, m.Hkv, m.D, pos, m.qw.cpu(), m.kw.cpu(), 1e-6, m.freq.cpu(), False, 1.0)
+        q = m.ws.q.cpu()[:rows].double()
+        bound = ref.BF16_HALF * want.abs() + 1.01 * ref.norm_rope_slack(size, m.D)
+        assert bool(((q - want[:rows, :m.Hq]).abs() <= bound[:rows, :m.Hq]).all())
+        c = m.cache
+        k, v = ref.k_rows(c.k.view(torch.uint8).cpu()).contiguous().view(FP8) if fp8 else ref.k_rows(c.k.cpu()), c.v.cpu()
+        k, v = ref.as_values(k, c.k_scale.cpu() if fp8 else None), ref.as_values(v, c.v_scale.cpu() if fp8 else None)
+        st = dict(q=m.ws.q.cpu(), k=k, v=v, table=m.table.cpu(), offs=m.plan.q_offsets.cpu().numpy(),
+                  lens=m.plan.kv_len.cpu().numpy(), page=m.page, D=m.D, rows=rows)
+        assert st["lens"].tolist() == [int(a) + b for a, b in zip(cached, new)]
+        o = m.ws.o.cpu()
+        want, mass, reach = ref.attention(st["q"], k, v, st["table"], st["offs"], st["lens"], m.page, m.D ** -0.5, 0.0, 0)
+        bound = ref.attention_bound(want, mass, reach, m.D, int(max(st["lens"])))
+        assert bool(((o.double() - want).abs() <= bound)[:rows].all())
+        want, size, y = ref.linear(o.view(m.T, -1), m.w_out.cpu(), None, None, m.x.cpu())
+        bound = ref.linear_bound(want, size, y, m.Hq * m.D, BF)
+        assert bool(((m.ws.out.cpu().double() - want).abs() <= bound)[:rows].all())
+        assert bool(torch.isfinite(m.y[:rows].float()).all())
+        m.advance()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_decode_steps_replay(fp8):
+    # one graph of a whole step, replayed while the lengths grow, against the same steps called one by one
+    steps = [[3, 1], [2, 3], [1, 1], [4, 0], [1, 1], [1, 1], [0, 5], [1, 1]] * 3
+    a, b = Model(fp8, 8), Model(fp8, 8)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        a.step()                                      # before any token: warms up, changes nothing
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            a.step()
+    torch.cuda.synchronize()
+    g = rng(33)
+    for new in steps:
+        x = torch.randn(8, 256, generator=g).to(BF).cuda()
+        for m in (a, b):
+            m.x.copy_(x)
+            m.new.copy_(ints(new))
+        graph.replay()
+        b.step()
+        torch.cuda.synchronize()
+        rows = sum(new)
+        assert torch.equal(a.plan.slots, b.plan.slots) and torch.equal(a.table, b.table)
+        assert torch.equal(a.y[:rows].view(torch.int16), b.y[:rows].view(torch.int16))
+        for m in (a, b):
+            m.advance()
+    assert int(a.cached.sum()) == sum(map(sum, steps))
+
+
+def test_two_captured_graphs_share_a_workspace_in_turn():
+    one = attn_state([2500], [2], 8, 1, 128, 16, False, seed=40)
+    two = attn_state([900, 40], [1, 1], 8, 1, 128, 16, False, seed=41)
+    alone = [run_attn(one), run_attn(two)]
+    ws = torch.empty(max(moe.paged_attention_workspace_size(st["T"], 8, 1, 128, len(st["lens"])) for st in (one, two)),
+                     dtype=torch.uint8, device="cuda")
+    graphs, outs, keep = [], [], []
+    for st in (one, two):
+        args = (st["q"].cuda(), st["cache"], st["table"].cuda(), ints(st["offs"]), ints(st["lens"]))
+        out = torch.empty_like(args[0])
+        moe.paged_attention(*args, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.paged_attention(*args, out=out, workspace=ws)
+        graphs.append(graph)
+        outs.append(out)
+        keep.append(args)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1, 0)):
+        for i in order:
+            outs[i].zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            assert torch.equal(outs[i].cpu().view(torch.int16), alone[i].view(torch.int16))
