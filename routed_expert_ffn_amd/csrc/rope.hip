@@ -15,6 +15,7 @@
 // 0.015 radians), the sine and cosine of the remainder in fp32.
 #include "attn.h"
 #include "common.h"
+#include "stream.h"
 
 #include <algorithm>
 
@@ -23,6 +24,19 @@ namespace {
 constexpr int ROPE_THREADS = 256;
 typedef uint32_t u32x2_r __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_r __attribute__((ext_vector_type(2)));
+
+// Sum over the LPH lanes of a head (8, 16 or 32), in every one of them: partners
+// by DPP within 16 lanes (each step's partner lies in the other half, whose
+// lanes already hold one value), across 16 by a lane swap.
+template <int LPH>
+MOE_DEV float head_sum(float v) {
+    v += tr_partner<1>(v);
+    v += tr_partner<2>(v);
+    v += tr_partner<4>(v);
+    if constexpr (LPH >= 16) v += tr_partner<8>(v);
+    if constexpr (LPH >= 32) v += tr_partner<16>(v);
+    return v;
+}
 
 MOE_DEV uint32_t pack2(float lo, float hi) {
     const bf16x2_r v = {(__bf16)lo, (__bf16)hi};
@@ -43,7 +57,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
     constexpr int LPH = D / 8;             // lanes per head
     constexpr int HPW = WAVE / LPH;        // heads per wave
     constexpr int NWV = ROPE_THREADS / WAVE;
-    __shared__ float2 cs[TB * (D / 2)];    // (cos, sin) * rope_scale of the block's rows
+    __shared__ __attribute__((aligned(16))) float2 cs[TB * (D / 2)];   // (cos, sin) * rope_scale of the block's rows
     __shared__ int row_slot[TB];
     const int t0 = blockIdx.x * TB;
     const int rows = min(TB, T - t0);
@@ -56,7 +70,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
     auto load = [&](int u) __attribute__((always_inline)) -> uint4 {
         u = min(u, units - 1);             // past the end: the last unit again, not used
         const int r = u / groups, h = min((g_begin + u - r * groups) * HPW + sub, heads - 1);
-        return *reinterpret_cast<const uint4*>(qkv + (int64_t)(t0 + r) * stride + h * D + c8 * 8);
+        return ldnt16(qkv + (int64_t)(t0 + r) * stride + h * D + c8 * 8);
     };
     uint4 raw[UN];
 #pragma unroll
@@ -97,14 +111,14 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
 #pragma unroll
         for (int i = 0; i < 4; i++) { x[2 * i] = bf16lo_to_f32(u4[i]); x[2 * i + 1] = bf16hi_to_f32(u4[i]); }
         const bool is_q = h < n_heads, is_v = h >= n_heads + nk;
+        const bool all_q = (g_begin + u - r * groups) * HPW + HPW <= n_heads;
         if (qn || kn) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; i++) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int d = 1; d < LPH; d <<= 1) ss += wave_xor(ss, d);
+            ss = head_sum<LPH>(ss);
+            const float inv = __builtin_amdgcn_rsqf(ss * (1.0f / D) + eps);
             if (!is_v && (is_q ? qn : kn)) {
-                const float inv = 1.0f / sqrtf(ss * (1.0f / D) + eps);
 #pragma unroll
                 for (int i = 0; i < 8; i++) x[i] = x[i] * inv * (is_q ? qw[i] : kw[i]);
             }
@@ -113,7 +127,8 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
             if (!is_v && turned) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float2 a = cs[r * (D / 2) + c8 * 4 + i];
+                    const float4 a2 = reinterpret_cast<const float4*>(cs + r * (D / 2) + c8 * 4)[i / 2];
+                    const float2 a = i % 2 ? make_float2(a2.z, a2.w) : make_float2(a2.x, a2.y);
                     const float p = x[2 * i], q = x[2 * i + 1];
                     x[2 * i] = p * a.x - q * a.y;
                     x[2 * i + 1] = q * a.x + p * a.y;
@@ -124,9 +139,14 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
 #pragma unroll
             for (int i = 0; i < 8; i++) y[i] = __shfl(x[i], pair_lane, WAVE);
             if (!is_v && turned) {
-                const float2* ang = cs + r * (D / 2) + pair_chunk * 8;
+                const float4* ang = reinterpret_cast<const float4*>(cs + r * (D / 2) + pair_chunk * 8);
+                const float sign = second ? 1.f : -1.f;
 #pragma unroll
-                for (int i = 0; i < 8; i++) x[i] = x[i] * ang[i].x + (second ? y[i] : -y[i]) * ang[i].y;
+                for (int i = 0; i < 4; i++) {
+                    const float4 a = ang[i];
+                    x[2 * i] = fmaf(x[2 * i], a.x, sign * y[2 * i] * a.y);
+                    x[2 * i + 1] = fmaf(x[2 * i + 1], a.z, sign * y[2 * i + 1] * a.w);
+                }
             }
         }
         if (is_q) {
@@ -134,7 +154,7 @@ __global__ __launch_bounds__(ROPE_THREADS) void k_qk_norm_rope(
             o.x = pack2(x[0], x[1]); o.y = pack2(x[2], x[3]); o.z = pack2(x[4], x[5]); o.w = pack2(x[6], x[7]);
             *reinterpret_cast<uint4*>(q_out + ((int64_t)t * n_heads + h) * D + c8 * 8) = o;
         }
-        if ((g_begin + u - r * groups) * HPW + HPW - 1 < n_heads) return;  // all of the wave's heads are q heads
+        if (all_q) return;
         const int kh = is_v ? h - n_heads - nk : h - n_heads;
         const int64_t ph = (int64_t)(slot >> cache.page_shift) * nk + kh;  // (page, head)
         const int off = slot & page_mask;
@@ -212,7 +232,7 @@ hipError_t launch_d(const uint16_t* qkv, int64_t stride, int T, int n_heads, con
     // 8 rows per block (their keys' 16-byte chunks fill whole lines), the heads
     // split until there are about 1024 blocks; few rows: one row and one group
     // of heads per wave
-    if ((int64_t)T * groups <= 4096)
+    if ((int64_t)T * groups <= 16384)
         launch_t<D, F8, 1, 1>(4, qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions,
                               slots, q_out, st);
     else
