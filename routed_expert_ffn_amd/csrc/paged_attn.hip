@@ -75,6 +75,7 @@ struct AttnArgs {
     uint16_t* out;
     int G;                                  // query heads per key-value head
     int G16;                                // ceil(2^16 / G): x / G = x G16 >> 16 for x < 1024
+    int whole;                              // no unit is split: each goes to the share that its first step lies in
     int shares;                             // blocks of the attention launch
     int* share;                             // [1] steps per share, written by block 0 for the join
     int* base;                              // [S] first step of each request
@@ -176,8 +177,8 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     int* base = (int*)smem;
     unsigned char* area = smem + (lanes ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16);
     uint16_t* qs = (uint16_t*)area;                              // [RB][QP]
-    float* ja = (float*)area;                                    // [PW][16][DP]
-    float2* jml = (float2*)(area + sizeof(float) * PW * 16 * DP);  // [PW][16]
+    float* ja = (float*)area;                                    // [PW][RB][DP]
+    float2* jml = (float2*)(area + sizeof(float) * PW * RB * DP);  // [PW][RB]
     __shared__ int sc32[NW];
     __shared__ int strange;                 // the piece met infinite or NaN values in a tile seen in part
 
@@ -270,7 +271,11 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         // the piece: steps [st0, st1) of unit (row group, head)
         const int unit = uniform((int)((uint32_t)(at - s_base) / (uint32_t)rq.steps));
         const int st0 = at - s_base - unit * rq.steps;
-        const int st1 = min(rq.steps, st0 + (share_hi - at));
+        if (a.whole && st0 > 0) {           // the share before has it
+            at += rq.steps - st0;
+            continue;
+        }
+        const int st1 = a.whole ? rq.steps : min(rq.steps, st0 + (share_hi - at));
         const int piece_at = at;
         at += st1 - st0;
         const int grp = uniform((int)((uint32_t)unit / (uint32_t)nkv)), head = unit - grp * nkv;
@@ -659,67 +664,78 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             }
         };
 
-        // ---- join the block's waves, one row tile at a time.  A unit that lies in
-        // this share alone is done; of others the piece that begins with the share
-        // is partial 2 b, one that begins inside it 2 b + 1.
-        // (The loop stays a loop: code that runs once per piece is paid for in
-        // instruction fetches, about 60 ns per 64 bytes.)
+        // ---- join the block's waves through LDS.  A unit that lies in this share
+        // alone is done; of others the piece that begins with the share is partial
+        // 2 b, one that begins inside it 2 b + 1.  (What runs once per piece is kept
+        // in loops: its code is paid for in instruction fetches, about 60 ns per 64
+        // bytes.)
         const bool direct = st1 - st0 == rq.steps;
         const int64_t pidx = 2 * (int64_t)blockIdx.x + (piece_at == share_lo ? 0 : 1);
-#pragma unroll 1
+        if (!QREG) lds_barrier();           // the q rows are read
+#pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            if (mt > 0 || !QREG) lds_barrier();     // the row tile before, or the q rows, are read
+            float sm = sum[mt];
+            sm += tr_partner<16>(sm);
+            sm += tr_partner<32>(sm);
+            if (g4 == 0 && wd == 0) jml[wp * RB + mt * 16 + r16] = make_float2(m[mt], sm);
+            // O^T rows 4 g4 + i of MFMA (h, e) are d = 16 E h + E (4 g4 + i) + e: kept
+            // in that order, (h, e, 4 g4 + i), here and in the partial results
 #pragma unroll
-            for (int k = 0; k < MT; k++) {
-                if (mt != k) continue;              // uniform
-                float sm = sum[k];
-                sm += tr_partner<16>(sm);
-                sm += tr_partner<32>(sm);
-                if (g4 == 0 && wd == 0) jml[wp * 16 + r16] = make_float2(m[k], sm);
-                // O^T rows 4 g4 + i of MFMA (h, e) are d = 16 E h + E (4 g4 + i) + e: kept
-                // in that order, (h, e, 4 g4 + i), here and in the partial results
+            for (int h = 0; h < NH; h++)
 #pragma unroll
-                for (int h = 0; h < NH; h++)
-#pragma unroll
-                    for (int e = 0; e < E; e++)
-                        *reinterpret_cast<f32x4_t*>(ja + (wp * 16 + r16) * DP + ((wd * NH + h) * E + e) * 16 + 4 * g4) = acc[k][h][e];
-            }
-            lds_barrier();
-            // 16 threads per row, D / 16 elements each, 4 at a time
-            const int rr = tid >> 4, part = tid & 15, row = mt * 16 + rr;
-            if (row < nrows) {
-                float2 x[PW];
-#pragma unroll
-                for (int i = 0; i < PW; i++) x[i] = jml[i * 16 + rr];
-                float Mr = x[0].x, L = 0.f, f[PW];
-#pragma unroll
-                for (int i = 1; i < PW; i++) Mr = fmaxf(Mr, x[i].x);
-                const float br = Mr == -__builtin_inff() ? 0.f : Mr;
-#pragma unroll
-                for (int i = 0; i < PW; i++) {
-                    f[i] = __builtin_amdgcn_exp2f(x[i].x - br);
-                    L += x[i].y * f[i];
-                }
-                const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);     // (a row that sees nothing: 0)
-                const int x0 = r_in + row, i = i0 + ((x0 * a.G16) >> 16), g = x0 - (i - i0) * G;
-                uint16_t* dst = a.out + ((int64_t)(rq.row0 + i) * a.n_heads + head * G + g) * D;
-                float* pd = a.part + (pidx * RB + row) * D;
-                const int odd = strange;
-#pragma unroll 1
+                for (int e = 0; e < E; e++)
+                    *reinterpret_cast<f32x4_t*>(ja + (wp * RB + mt * 16 + r16) * DP + ((wd * NH + h) * E + e) * 16 + 4 * g4) =
+                        acc[mt][h][e];
+        }
+        lds_barrier();
+        // 16 threads per row, D / 16 elements each, 4 at a time
+        const int rr = tid >> 4, part = tid & 15;
+        if (strange) {
+            for (int row = rr; row < nrows; row += 16) {
+                int top = 0;                // a wave whose sums enter unscaled
+                for (int i = 1; i < PW; i++) top = jml[i * RB + row].x > jml[top * RB + row].x ? i : top;
+                const int p = rq.first + i0 + (((r_in + row) * a.G16) >> 16);
                 for (int c = part; c < D / 4; c += 16) {
-                    const float* src = ja + rr * DP + c * 4;
-                    f32x4_t o = *reinterpret_cast<const f32x4_t*>(src) * f[0];
-#pragma unroll
-                    for (int i2 = 1; i2 < PW; i2++) o += *reinterpret_cast<const f32x4_t*>(src + i2 * 16 * DP) * f[i2];
-                    if (odd) add_strange(o, rq.first + i, dim_of<D>(c), E);
-                    if (direct) {
-#pragma unroll
-                        for (int q = 0; q < 4; q++) dst[dim_of<D>(c) + E * q] = (uint16_t)pk_bf16(o[q] * inv, 0.f);
-                    } else {
-                        *reinterpret_cast<f32x4_t*>(pd + c * 4) = o;
-                    }
+                    f32x4_t* o = reinterpret_cast<f32x4_t*>(ja + (top * RB + row) * DP + c * 4);
+                    f32x4_t v = *o;
+                    add_strange(v, p, dim_of<D>(c), E);
+                    *o = v;
                 }
-                if (!direct && part == 0) a.ml[pidx * RB + row] = make_float2(Mr, L);
+            }
+        }
+#pragma unroll 1
+        for (int row = rr; row < nrows; row += 16) {
+            float2 x[PW];
+#pragma unroll
+            for (int i = 0; i < PW; i++) x[i] = jml[i * RB + row];
+            f32x4_t o[D / 64];
+#pragma unroll
+            for (int c = 0; c < D / 64; c++) o[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            float Mr = x[0].x, L = 0.f;
+#pragma unroll
+            for (int i = 1; i < PW; i++) Mr = fmaxf(Mr, x[i].x);
+            const float br = Mr == -__builtin_inff() ? 0.f : Mr;
+#pragma unroll
+            for (int i = 0; i < PW; i++) {
+                const float f = __builtin_amdgcn_exp2f(x[i].x - br);
+                L += x[i].y * f;
+#pragma unroll
+                for (int c = 0; c < D / 64; c++)
+                    o[c] += *reinterpret_cast<const f32x4_t*>(ja + (i * RB + row) * DP + (c * 16 + part) * 4) * f;
+            }
+            if (direct) {
+                const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);     // (a row that sees nothing: 0)
+                const int x0 = r_in + row, i = (x0 * a.G16) >> 16, g = x0 - i * G;
+                uint16_t* dst = a.out + ((int64_t)(rq.row0 + i0 + i) * a.n_heads + head * G + g) * D;
+#pragma unroll
+                for (int c = 0; c < D / 64; c++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) dst[dim_of<D>(c * 16 + part) + E * q] = (uint16_t)pk_bf16(o[c][q] * inv, 0.f);
+            } else {
+                float* pd = a.part + (pidx * RB + row) * D;
+#pragma unroll
+                for (int c = 0; c < D / 64; c++) *reinterpret_cast<f32x4_t*>(pd + (c * 16 + part) * 4) = o[c];
+                if (part == 0) a.ml[pidx * RB + row] = make_float2(Mr, L);
             }
         }
     }
@@ -857,14 +873,15 @@ hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     using SH = Shape<D, F8, MT>;
     auto kern = k_paged_attn<D, F8, MT>;
     const size_t head = a.S <= WAVE ? 0 : ((size_t)a.S * 4 + 15) / 16 * 16;
-    const size_t join = (sizeof(float) * 16 * (D + 4) + sizeof(float2) * 16) * (NW / SH::DS);
+    const size_t join = (sizeof(float) * (D + 4) + sizeof(float2)) * 16 * MT * (NW / SH::DS);
     const size_t qrows = SH::QREG ? 0 : (size_t)16 * MT * (D + 8) * 2;
     const size_t lds = head + (join > qrows ? join : qrows);
     static LdsLimit lim;
-    hipError_t e = lim.ensure((const void*)kern, 128 * 1024);
+    hipError_t e = lim.ensure((const void*)kern, 156 * 1024);
     if (e != hipSuccess) return e;
     a.shares = shares_of(D, MT);
     hipLaunchKernelGGL(kern, dim3(a.shares), dim3(AT_THREADS), lds, st, a);
+    if (a.whole) return hipGetLastError();
     const int64_t chunks = (int64_t)a.T * a.n_heads * (D / 64);
     auto launch_join = [&](auto kern, dim3 grid, int threads) { hipLaunchKernelGGL(kern, grid, dim3(threads), 0, st, a); };
     if (chunks <= 128) launch_join(k_attn_join<D, 16 * MT, SH::STEP, 64, 16>, dim3(a.T, a.n_heads * (D / 64)), 16 * WAVE);
@@ -901,6 +918,9 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     a.q = q; a.q_stride = q_stride; a.T = T; a.n_heads = n_heads; a.kv = cache;
     a.table = table; a.W = W; a.q_offsets = q_offsets; a.kv_len = kv_len; a.S = S;
     a.scale = scale; a.softcap = softcap; a.window = window; a.out = out;
+    // contexts of up to 512 positions are at most a few steps long: no splitting,
+    // and no second launch (one to eight such requests: 14 -> 8 us a call)
+    a.whole = (int64_t)W << cache.page_shift <= 512;
     a.share = (int*)wb; a.base = (int*)wb + 1;
     a.G = n_heads / cache.n_kv_heads; a.G16 = (65536 + a.G - 1) / a.G;
     a.ml = (float2*)(wb + L.ml); a.part = (float*)(wb + L.part);
