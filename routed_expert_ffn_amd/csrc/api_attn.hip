@@ -4,6 +4,8 @@
 #include "../../include/moe.h"
 #include "attn.h"
 
+#include <cmath>
+
 namespace {
 
 bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
@@ -60,7 +62,8 @@ moe_status moe_qk_norm_rope(const void* qkv, int32_t x_dtype, int64_t qkv_stride
                             const moe_kv_cache* cache, const float* q_weight, const float* k_weight, float eps,
                             const float* inv_freq, int32_t rope_dim, int32_t rope_layout, float rope_scale,
                             const int32_t* positions, const int32_t* slots, void* q_out, moe_stream stream) {
-    if (T < 0 || n_heads <= 0 || rope_dim < 0) return MOE_ERR_INVALID_ARG;
+    if (T < 0 || n_heads <= 0 || rope_dim < 0 || !(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(rope_scale))
+        return MOE_ERR_INVALID_ARG;
     if (x_dtype != MOE_F32 && x_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (rope_layout != MOE_ROPE_HALF && rope_layout != MOE_ROPE_INTERLEAVED) return MOE_ERR_INVALID_ARG;
     KvView kv;
@@ -88,13 +91,15 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
                           const moe_kv_cache* cache, const int32_t* page_table, int32_t W, const int32_t* q_offsets,
                           const int32_t* kv_len, int32_t S_, float scale, float softcap, int32_t window, void* out,
                           void* workspace, size_t ws_bytes, moe_stream stream) {
-    if (T < 0 || n_heads <= 0 || W <= 0 || S_ <= 0 || window < 0 || !(softcap >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (T < 0 || n_heads <= 0 || W <= 0 || S_ <= 0 || window < 0 || !(softcap >= 0.0f) || !std::isfinite(softcap) ||
+        !std::isfinite(scale))
+        return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_F32 && q_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     KvView kv;
     const moe_status chk = cache_view(cache, &kv);
     if (chk != MOE_OK) return chk;
     if (!page_table || !q_offsets || !kv_len || (T > 0 && (!q || !out))) return MOE_ERR_INVALID_ARG;
-    if (q_stride < (int64_t)n_heads * kv.head_dim || (int64_t)T * n_heads > INT32_MAX) return MOE_ERR_INVALID_ARG;
+    if (q_stride < (int64_t)n_heads * kv.head_dim || (int64_t)T * n_heads > (int64_t)1 << 30) return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_BF16 || S_ > MAX_REQUESTS || n_heads % kv.n_kv_heads != 0 ||
         n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)n_heads * kv.head_dim > 64 * 65535 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
         return MOE_ERR_UNSUPPORTED;

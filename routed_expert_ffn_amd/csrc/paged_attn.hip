@@ -94,7 +94,7 @@ template <int RB, int STEP>
 MOE_DEV Request request_of(const AttnArgs& a, int s) {
     Request r;
     const int b = min(max(a.q_offsets[s], 0), a.T), e = min(max(a.q_offsets[s + 1], 0), a.T);
-    const int L = max(a.kv_len[s], 0);
+    const int L = min(max(a.kv_len[s], 0), 1 << 30);
     r.row0 = b;
     r.n = max(e - b, 0);
     r.first = L - r.n;
@@ -917,7 +917,8 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     AttnArgs a{};
     a.q = q; a.q_stride = q_stride; a.T = T; a.n_heads = n_heads; a.kv = cache;
     a.table = table; a.W = W; a.q_offsets = q_offsets; a.kv_len = kv_len; a.S = S;
-    a.scale = scale; a.softcap = softcap; a.window = window; a.out = out;
+    a.scale = scale; a.softcap = softcap; a.out = out;
+    a.window = window >= 1 << 30 ? 0 : window;     // positions stay below 2^30: no window
     // contexts of up to 512 positions are at most a few steps long: no splitting,
     // and no second launch (one to eight such requests: 14 -> 8 us a call)
     a.whole = (int64_t)W << cache.page_shift <= 512;

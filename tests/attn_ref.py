@@ -82,7 +82,7 @@ def attention(q, k, v, table, offs, lens, page, scale, softcap, window):
                 w = torch.softmax(x, 0)
                 out[a + i, h] = w @ vv
                 mass[a + i, h] = w @ vv.abs()
-                reach[a + i, h] = (kk.abs() @ qq.abs()).max() * scale
+                reach[a + i, h] = (kk.abs() @ qq.abs()).max() * abs(scale)
     return out, mass, reach
 
 

@@ -51,17 +51,21 @@ def test_kv_plan_refuses(L):
 
 def test_qk_norm_rope_refuses(L):
     base = dict(x=FAKE, xd=moe.BF16, st=20 * 128, T=3, h=16, c=cache(), qw=FAKE, kw=FAKE, f=FAKE, R=64, lay=0, p=FAKE,
-                s=FAKE, o=FAKE)
+                s=FAKE, o=FAKE, eps=1e-6, rs=1.0)
 
     def call(**kw):
         a = dict(base, **kw)
         return L.moe_qk_norm_rope(a["x"], a["xd"], a["st"], a["T"], a["h"], ctypes.byref(a["c"]) if a["c"] else None,
-                                  a["qw"], a["kw"], 1e-6, a["f"], a["R"], a["lay"], 1.0, a["p"], a["s"], a["o"], None)
+                                  a["qw"], a["kw"], a["eps"], a["f"], a["R"], a["lay"], a["rs"], a["p"], a["s"], a["o"],
+                                  None)
     for kw, status in CACHES:
         assert call(c=cache(**kw)) == status, kw
     for name in ("x", "c", "f", "p", "s", "o"):
         assert call(**{name: None}) == INVALID, name
     assert call(T=-1) == INVALID and call(h=0) == INVALID and call(lay=2) == INVALID and call(xd=7) == INVALID
+    for bad in (float("nan"), float("inf")):
+        assert call(eps=bad) == INVALID and call(rs=bad) == INVALID
+    assert call(eps=-1e-6) == INVALID
     assert call(R=-16) == INVALID and call(R=144) == INVALID and call(st=20 * 128 - 8) == INVALID
     assert call(xd=moe.F32) == UNSUPPORTED and call(R=24) == UNSUPPORTED and call(st=20 * 128 + 4) == UNSUPPORTED
     assert call(h=1021, st=1025 * 128) == UNSUPPORTED
@@ -71,12 +75,12 @@ def test_qk_norm_rope_refuses(L):
 def test_paged_attn_refuses(L):
     nb = moe.paged_attention_workspace_size(3, 16, 2, 128, 2)
     base = dict(q=FAKE, qd=moe.BF16, st=16 * 128, T=3, h=16, c=cache(), t=FAKE, W=4, o=FAKE, k=FAKE, S=2, cap=0.0,
-                win=0, out=FAKE, ws=FAKE, nb=nb)
+                win=0, out=FAKE, ws=FAKE, nb=nb, sc=0.1)
 
     def call(**kw):
         a = dict(base, **kw)
         return L.moe_paged_attn(a["q"], a["qd"], a["st"], a["T"], a["h"], ctypes.byref(a["c"]) if a["c"] else None,
-                                a["t"], a["W"], a["o"], a["k"], a["S"], 0.1, a["cap"], a["win"], a["out"], a["ws"],
+                                a["t"], a["W"], a["o"], a["k"], a["S"], a["sc"], a["cap"], a["win"], a["out"], a["ws"],
                                 a["nb"], None)
     for kw, status in CACHES:
         assert call(c=cache(**kw)) == status, kw
@@ -84,7 +88,9 @@ def test_paged_attn_refuses(L):
         assert call(**{name: None}) == INVALID, name
     assert call(T=-1) == INVALID and call(S=0) == INVALID and call(W=0) == INVALID and call(win=-1) == INVALID
     assert call(cap=-1.0) == INVALID and call(cap=float("nan")) == INVALID and call(qd=9) == INVALID
-    assert call(st=8) == INVALID
+    for bad in (float("nan"), float("inf")):
+        assert call(cap=bad) == INVALID and call(sc=bad) == INVALID
+    assert call(st=8) == INVALID and call(T=1 << 27, h=16, c=cache()) == INVALID
     assert call(qd=moe.F32) == UNSUPPORTED and call(S=4097) == UNSUPPORTED and call(h=15) == UNSUPPORTED
     assert call(h=130, st=130 * 128) == UNSUPPORTED                        # 65 query heads per key-value head
     assert call(st=16 * 128 + 4) == UNSUPPORTED and call(W=1 << 27) == UNSUPPORTED and call(q=ODD) == UNSUPPORTED

@@ -154,6 +154,31 @@ def test_qk_norm_rope(case):
             assert bool(((val - y).abs() <= tol).all()), name
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_qk_norm_rope_keeps_infinities_in_their_head(fp8):
+    T, Hq, Hkv, D = 3, 2, 2, 64
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=rng(50)).to(BF)
+    clean = qkv.clone()
+    qkv[0, 0, 3], qkv[1, 2, 5], qkv[2, 5, 7] = math.nan, math.inf, math.inf           # a q, a k and a v head
+    outs = []
+    for x in (clean, qkv):
+        cache = moe.KVCache.allocate(1, 16, Hkv, D, FP8 if fp8 else BF)
+        for t in (cache.k, cache.v):
+            t.view(torch.uint8).fill_(0)
+        q = moe.qk_norm_rope(x.view(T, -1).cuda(), cache, ints([0, 1, 2]), ints([0, 1, 2]),
+                             torch.ones(D, device="cuda"), torch.ones(D, device="cuda"))
+        torch.cuda.synchronize()
+        rows = ref.k_rows(cache.k.view(torch.uint8).cpu()).contiguous().view(FP8) if fp8 else ref.k_rows(cache.k.cpu())
+        k = ref.as_values(rows, cache.k_scale.cpu() if fp8 else None)[0, :, :3]
+        v = ref.as_values(cache.v.cpu(), cache.v_scale.cpu() if fp8 else None)[0, :, :3]
+        outs.append((q.cpu().double(), k, v))
+    for name, a, b, bad in zip("qkv", *outs, ((0, 0), (0, 1), (1, 2))):
+        same = torch.ones(a.shape[:2], dtype=torch.bool)
+        same[bad] = False
+        assert torch.equal(a[same], b[same]), name
+        assert not bool(torch.isfinite(b[bad]).all()), name
+
+
 # ---------------------------------------------------------------- paged attention
 def attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=0, pad=0, W=None, spare=3, poison=True):
     """q, a cache whose unused places hold NaN, a page table whose unused entries are garbage."""
@@ -267,6 +292,23 @@ def test_paged_attention_rows_that_see_nothing(fp8):
     got = run_attn(st, table=table)
     check_attn(st, got, table=table)
     assert bool((got[0] == 0).all()) and bool((got[1:4] == 0).all()) and bool((got[6] == 0).all())
+
+
+def test_paged_attention_windows_of_one_and_of_everything():
+    st = attn_state([200, 5], [7, 5], 4, 2, 64, 16, False, seed=9)
+    check_attn(st, run_attn(st, window=1), window=1)
+    a = run_attn(st)
+    for w in (200, 1 << 30, (1 << 31) - 1):
+        assert torch.equal(run_attn(st, window=w).view(torch.int16), a.view(torch.int16))
+
+
+def test_paged_attention_scale_of_zero_and_below():
+    st = attn_state([90, 700], [3, 1], 4, 2, 64, 16, True, seed=10)
+    for scale in (0.0, -0.3):
+        got = run_attn(st, scale=scale)
+        want, mass, reach = ref.attention(st["q"], st["k"], st["v"], st["table"], st["offs"], st["lens"], 16, scale, 0.0, 0)
+        bound = ref.attention_bound(want, mass, reach.abs(), 64, 700)
+        assert bool(((got.double() - want).abs() <= bound).all())
 
 
 def test_paged_attention_lengths_past_the_table():
