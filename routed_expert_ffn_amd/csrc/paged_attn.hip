@@ -58,7 +58,7 @@ MOE_DEV uint32_t fp8x2_bf16(uint32_t w) {
 
 // What a piece costs besides its own positions (its q rows, first loads and
 // join), in positions: short requests would otherwise pile up in few shares.
-constexpr int PIECE_COST = 256;
+constexpr int PIECE_COST = 128;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -154,7 +154,7 @@ struct Shape {
     // half of the head: half the accumulators, and half the planes to join.
     static constexpr int DS = D == 256 && MT > 1 ? 2 : 1;
     // sub-tiles per wave step: 16 KB of cache in flight per wave (8 KB of e4m3), by registers
-    static constexpr int NSUB = D == 256 && !F8 ? 1 : 2;
+    static constexpr int NSUB = D == 256 && (MT == 2 || (MT == 1 && !F8)) ? 1 : 2;
     static constexpr int STEP = 16 * NSUB * NW / DS;    // positions per block step
     static constexpr bool QREG = D * MT <= 128;     // q fragments in registers (up to 16 of them), else LDS at each use
 };
@@ -414,11 +414,14 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         }
 
         f32x4_t acc[MT][NH][E];
-        float m[MT], sum[MT];
+        // running sums of the weights: bf16 values, a row of ones of the second
+        // product (the whole sum in every lane); e4m3, this lane's positions
+        float m[MT];
+        f32x4_t sum[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             m[mt] = -__builtin_inff();
-            sum[mt] = 0.f;
+            sum[mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int h = 0; h < NH; h++)
 #pragma unroll
@@ -467,6 +470,18 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         };
         auto values = [&](const TL& t, const uint32_t (&p)[MT][2 * NSUB]) __attribute__((always_inline)) {
             constexpr int PER = F8 ? 4 : 2;               // elements per word
+            if constexpr (!F8) {
+                uint32_t one[JP];
+#pragma unroll
+                for (int j = 0; j < JP; j++) one[j] = 0x3F803F80u;
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    uint32_t pp[JP];
+#pragma unroll
+                    for (int j = 0; j < JP; j++) pp[j] = p[mt][j];
+                    sum[mt] = mma(one, pp, sum[mt]);
+                }
+            }
 #pragma unroll
             for (int pr = 0; pr < 2 * NSUB / JP; pr++)
 #pragma unroll
@@ -500,30 +515,52 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                         }
                     }
         };
-        // running maximum of one row tile; sc -> probabilities
-        auto soften = [&](f32x4_t (&sc)[NSUB], int mt) __attribute__((always_inline)) {
-            float top = -__builtin_inff();
+        // running maxima; scores -> probabilities.  The row tiles go together (one
+        // branch, independent chains).
+        auto soften = [&](f32x4_t (&sc)[MT][NSUB]) __attribute__((always_inline)) {
+            float top[MT];
+            bool rise = false;
 #pragma unroll
-            for (int sb = 0; sb < NSUB; sb++)
-                top = fmaxf(top, fmaxf(fmaxf(sc[sb][0], sc[sb][1]), fmaxf(sc[sb][2], sc[sb][3])));
-            top = fmaxf(top, tr_partner<16>(top));
-            top = fmaxf(top, tr_partner<32>(top));
-            const float mn = fmaxf(m[mt], top);
-            const float base2 = mn == -__builtin_inff() ? 0.f : mn;      // a row that has seen nothing yet
-            // (nothing to scale before the first tile that a row sees)
-            if (__any(mn > m[mt] && m[mt] > -__builtin_inff())) {
-                const float f = __builtin_amdgcn_exp2f(m[mt] - base2);
-                sum[mt] *= f;
+            for (int mt = 0; mt < MT; mt++) {
+                float t = -__builtin_inff();
 #pragma unroll
-                for (int h = 0; h < NH; h++)
-#pragma unroll
-                    for (int e = 0; e < E; e++) acc[mt][h][e] *= f;
+                for (int sb = 0; sb < NSUB; sb++)
+                    t = fmaxf(t, fmaxf(fmaxf(sc[mt][sb][0], sc[mt][sb][1]), fmaxf(sc[mt][sb][2], sc[mt][sb][3])));
+                t = fmaxf(t, tr_partner<16>(t));
+                top[mt] = fmaxf(t, tr_partner<32>(t));
+                rise |= top[mt] > m[mt] + 8.f;
             }
-            m[mt] = mn;
+            // The base of the exponentials follows a row's maximum only when some row's
+            // has risen by more than 2^8: until then its probabilities grow to 256 at
+            // most, as exact as below 1, and nothing is scaled.
+            if (__any(rise)) {
+                bool seen = false;
 #pragma unroll
-            for (int sb = 0; sb < NSUB; sb++)
+                for (int mt = 0; mt < MT; mt++) seen |= m[mt] > -__builtin_inff();
+                const bool scale = __any(seen);              // (nothing to scale before the first tile that a row sees)
 #pragma unroll
-                for (int i = 0; i < 4; i++) sc[sb][i] = __builtin_amdgcn_exp2f(sc[sb][i] - base2);
+                for (int mt = 0; mt < MT; mt++) {
+                    const float mn = fmaxf(m[mt], top[mt]);
+                    if (scale) {
+                        const float f = __builtin_amdgcn_exp2f(m[mt] - (mn == -__builtin_inff() ? 0.f : mn));
+                        if constexpr (F8) sum[mt][0] *= f;
+                        else sum[mt] *= f;
+#pragma unroll
+                        for (int h = 0; h < NH; h++)
+#pragma unroll
+                            for (int e = 0; e < E; e++) acc[mt][h][e] *= f;
+                    }
+                    m[mt] = mn;
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+                const float base = m[mt] == -__builtin_inff() ? 0.f : m[mt];     // a row that has seen nothing yet
+#pragma unroll
+                for (int sb = 0; sb < NSUB; sb++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) sc[mt][sb][i] = __builtin_amdgcn_exp2f(sc[mt][sb][i] - base);
+            }
         };
         // the second product's operand, and the running sum of the weights as that
         // product sees them: the sum of the rounded probabilities, so that their
@@ -539,13 +576,14 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                     for (int i = 0; i < 4; i++) v[i] = v[i] == 0.f ? 0.f : v[i] * t.vs[sb][i];
                 p[2 * sb] = pk_bf16(v[0], v[1]);
                 p[2 * sb + 1] = pk_bf16(v[2], v[3]);
-                f32x4_t u = {bf16lo_to_f32(p[2 * sb]), bf16hi_to_f32(p[2 * sb]), bf16lo_to_f32(p[2 * sb + 1]),
-                             bf16hi_to_f32(p[2 * sb + 1])};
-                if constexpr (F8)
+                if constexpr (F8) {
+                    f32x4_t u = {bf16lo_to_f32(p[2 * sb]), bf16hi_to_f32(p[2 * sb]), bf16lo_to_f32(p[2 * sb + 1]),
+                                 bf16hi_to_f32(p[2 * sb + 1])};
 #pragma unroll
                     for (int i = 0; i < 4; i++)
                         u[i] = u[i] == 0.f ? sc[sb][i] : u[i] * __builtin_amdgcn_rcpf(t.vs[sb][i]);
-                sum[mt] += (u[0] + u[1]) + (u[2] + u[3]);
+                    sum[mt][0] += (u[0] + u[1]) + (u[2] + u[3]);
+                }
             }
         };
         // position of this lane's j-th value of the tile
@@ -609,24 +647,21 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             f32x4_t sc[MT][NSUB];
             if constexpr (!QREG) asm volatile("" ::: "memory");   // the q fragments are read again for every tile
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) {
-                scores(t, mt, sc[mt]);
-                if constexpr (!QREG) __builtin_amdgcn_sched_barrier(0);   // one row tile's q fragments at a time
-            }
+            for (int mt = 0; mt < MT; mt++) scores(t, mt, sc[mt]);
             load_k(t, t0 + STEP, pg_next);
-            uint32_t p[MT][2 * NSUB];
+            if (!whole) {
 #pragma unroll
-            for (int mt = 0; mt < MT; mt++) {
-                if (!whole) {
+                for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                     for (int j = 0; j < 4 * NSUB; j++) {
                         const int pos = pos_of(t0, j);
                         if (!((there >> j) & 1) || pos < vlo[mt] || pos > vhi[mt]) sc[mt][j >> 2][j & 3] = -__builtin_inff();
                     }
-                }
-                soften(sc[mt], mt);
-                pack_p(t, sc[mt], mt, p[mt]);
             }
+            soften(sc);
+            uint32_t p[MT][2 * NSUB];
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) pack_p(t, sc[mt], mt, p[mt]);
             values(t, p);
             load_v(t, t0 + STEP, pg_next);
             pg = pg_next;
@@ -674,9 +709,11 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         if (!QREG) lds_barrier();           // the q rows are read
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            float sm = sum[mt];
-            sm += tr_partner<16>(sm);
-            sm += tr_partner<32>(sm);
+            float sm = sum[mt][0];
+            if constexpr (F8) {
+                sm += tr_partner<16>(sm);
+                sm += tr_partner<32>(sm);
+            }
             if (g4 == 0 && wd == 0) jml[wp * RB + mt * 16 + r16] = make_float2(m[mt], sm);
             // O^T rows 4 g4 + i of MFMA (h, e) are d = 16 E h + E (4 g4 + i) + e: kept
             // in that order, (h, e, 4 g4 + i), here and in the partial results
