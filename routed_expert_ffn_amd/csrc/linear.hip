@@ -57,6 +57,13 @@ MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 // cores idle), and in return the loads need neither LDS nor narrow rows.
 // All of a block's loads go out at once.
 // More than 16 rows: TT tiles of 16, each with its own second operands and results.
+//   Bound: the weight's bytes, cold (a decode step reads each weight once).
+// 5 x 5120 x 2048: 21 MB in 6.1 us, 3.4 TB/s, of which about 2.5 us are the launch and
+// the first load's way to memory and back; the library's product of the same size
+// is 8.9.
+//   KS (k steps per wave and pass): as many as give one pass, so that all loads are
+// out at once, up to 4 (more would spill): K = 2048, two passes of KS 1 7.0 us, one of
+// KS 2 6.1.
 constexpr int ROWS_MAX_T = 32;
 constexpr int RW = 8;                      // waves per block
 
@@ -150,6 +157,15 @@ __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __
 // into the 16 slots of 256 bytes (lanes 0-3, 12-15 and 20-27 are served together,
 // 4-11, 16-19 and 28-31, and so on): BK 64, chunk ^ ((row >> 1) & 7); BK 32, chunk ^
 // {0, 2, 3, 1}[(row >> 2) & 3].  No conflicts counted.
+//   KG 2: two groups of waves take half of each K step each and add their sums at
+// the end through LDS: with one block per CU twice the waves hide what a K step
+// waits for.  48 x 1000 x 8192: 33 us with one group, 21 with two; at K = 512 the
+// adding costs more than it gives (4.7 us against 5.1).
+//   Bound: with many tiles the matrix cores and their feeding.  8192 x 2048 x 4096
+// 115 us, 1.19 PFLOP/s (1.36 PFLOP/s is what a large library product reaches; its
+// own time here is 92); 8 waves of 128 x 64 outputs each, two per SIMD, so that one
+// issues MFMAs while the other waits at the barrier (4 waves of 128 x 128 reach 1.1 at
+// best).  With few tiles the latency of a K step, 0.37 us per 128 of k and group.
 //   Blocks: tiles of one XCD (block mod 8) are neighbours, in panels of 8 column
 // tiles, so that they share x and w in its L2.
 // s_waitcnt vmcnt(N) lgkmcnt(0): this wave's older loads have landed, its LDS reads
@@ -161,9 +177,9 @@ MOE_DEV void wait_vm() {
 }
 MOE_DEV void dma16(const void* g, lds_ptr* l) { __builtin_amdgcn_global_load_lds(g, l, 16, 0, 0); }
 
-template <int BT, int BN, int BK, int ST, int WN>
+template <int BT, int BN, int BK, int ST, int WN, int KG>
 struct TileGeo {
-    static constexpr int NWV = 2 * WN;                       // waves: 2 along the rows, WN along the columns
+    static constexpr int NWV = 2 * WN * KG;                  // waves: 2 along the rows, WN along the columns, KG along k
     static constexpr int WT = BT / 2, WNC = BN / WN;         // a wave's rows and columns
     static constexpr int IT = WT / 16, JT = WNC / 16;        // its MFMA tiles
     static constexpr int ROWB = BK * 2;                      // LDS row bytes
@@ -172,20 +188,21 @@ struct TileGeo {
     static constexpr int DX = BT / RPI / NWV, DW = BN / RPI / NWV, DMA = DX + DW;   // per wave
     static_assert(DX * RPI * NWV == BT && DW * RPI * NWV == BN, "whole DMA instructions per wave");
     // epilogue: 32 rows x WNC columns fp32 per wave, rows padded by 16 bytes
-    static constexpr int EROW = WNC * 4 + 16, EPI = NWV * 32 * EROW;
-    static constexpr int LDS = STAGE * ST > EPI ? STAGE * ST : EPI;
+    static constexpr int EROW = WNC * 4 + 16, EPI = 2 * WN * 32 * EROW;
+    static constexpr int XCH = KG > 1 ? (KG - 1) * 2 * WN * IT * JT * 1024 : 0;      // sums of the other k groups
+    static constexpr int LDS = STAGE * ST > EPI + XCH ? STAGE * ST : EPI + XCH;
 };
 
-template <int BT, int BN, int BK, int ST, int WN, int OB, int BPC>
-__global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(const uint16_t* __restrict__ x, int x_stride,
+template <int BT, int BN, int BK, int ST, int WN, int KG, int OB, int BPC>
+__global__ __launch_bounds__(2 * WN * KG * WAVE, BPC * WN * KG / 2) void k_linear_tile(const uint16_t* __restrict__ x, int x_stride,
                                                                    const uint16_t* __restrict__ w,
                                                                    const float* __restrict__ bias, int act,
                                                                    const void* residual, int T, int N, int K, int tiles_t,
                                                                    int tiles_n, void* out) {
-    using G = TileGeo<BT, BN, BK, ST, WN>;
-    constexpr int IT = G::IT, JT = G::JT, KQ = BK / 32;      // MFMA steps per K step
+    using G = TileGeo<BT, BN, BK, ST, WN, KG>;
+    constexpr int IT = G::IT, JT = G::JT, KQ = BK / 32 / KG; // MFMA steps per K step and wave
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), wt = wv / WN, wn = wv % WN;
+    const int l = lane_id(), wv = uni(threadIdx.x / WAVE), kg = wv / (2 * WN), w4 = wv % (2 * WN), wt = w4 / WN, wn = w4 % WN;
     // tile of this block
     const int tiles = tiles_t * tiles_n, per = (tiles + 7) / 8;
     const int id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
@@ -200,7 +217,7 @@ __global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(con
     // holds global chunk (l % CPR) ^ swizzle(row).  Rows past the end repeat the last.
     constexpr int CPR = G::ROWB / 16;
     auto swz = [](int row) __attribute__((always_inline)) {
-        return BK == 64 ? (row >> 1) & 7 : (((row >> 2) ^ (row >> 3)) & 1) * 2 + ((row >> 3) & 1);
+        return BK == 128 ? row & 15 : BK == 64 ? (row >> 1) & 7 : (((row >> 2) ^ (row >> 3)) & 1) * 2 + ((row >> 3) & 1);
     };
     const unsigned char* xb = (const unsigned char*)(x + t0 * x_stride);
     const unsigned char* wb = (const unsigned char*)(w + (int64_t)n0 * K);
@@ -215,15 +232,25 @@ __global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(con
         const int r = (wv * G::DW + i) * G::RPI + l / CPR;
         wo[i] = (uint32_t)min(r, rows_n - 1) * (uint32_t)(K * 2) + (uint32_t)(((l % CPR) ^ swz(r)) * 16);
     }
-    const int nk = K / BK;
+    const int nk = K / BK;                  // whole steps; BK 128: K may leave half a step over
+    const bool rest = BK == 128 && K % BK != 0;
+    const int last = rest ? nk : nk - 1;
     auto issue = [&](int k) __attribute__((always_inline)) {
         unsigned char* st = smem + (k % ST) * G::STAGE;
-        k = min(k, nk - 1);
+        k = min(k, last);
+        // (in the half step the second half's lanes load the first half again, unused)
 #pragma unroll
-        for (int i = 0; i < G::DX; i++) dma16(xb + (int64_t)k * G::ROWB + xo[i], (lds_ptr*)(st + (wv * G::DX + i) * 1024));
+        for (int i = 0; i < G::DX; i++) {
+            uint32_t o = xo[i];
+            if (BK == 128 && rest && k == nk && (((l % CPR) ^ swz((wv * G::DX + i) * G::RPI + l / CPR)) >= 8)) o -= 128;
+            dma16(xb + (int64_t)k * G::ROWB + o, (lds_ptr*)(st + (wv * G::DX + i) * 1024));
+        }
 #pragma unroll
-        for (int i = 0; i < G::DW; i++)
-            dma16(wb + (int64_t)k * G::ROWB + wo[i], (lds_ptr*)(st + BT * G::ROWB + (wv * G::DW + i) * 1024));
+        for (int i = 0; i < G::DW; i++) {
+            uint32_t o = wo[i];
+            if (BK == 128 && rest && k == nk && (((l % CPR) ^ swz((wv * G::DW + i) * G::RPI + l / CPR)) >= 8)) o -= 128;
+            dma16(wb + (int64_t)k * G::ROWB + o, (lds_ptr*)(st + BT * G::ROWB + (wv * G::DW + i) * 1024));
+        }
     };
     const int fr = l & 15, fh = l >> 4;
     struct Frag { bf16x8_t x[IT][KQ], w[JT][KQ]; };
@@ -231,7 +258,7 @@ __global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(con
         const unsigned char* st = smem + (k % ST) * G::STAGE;
 #pragma unroll
         for (int q = 0; q < KQ; q++) {
-            const int c = q * 4 + fh;
+            const int c = (kg * KQ + q) * 4 + fh;
 #pragma unroll
             for (int i = 0; i < IT; i++) {
                 const int r = wt * G::WT + i * 16 + fr;
@@ -293,14 +320,33 @@ __global__ __launch_bounds__(2 * WN * WAVE, BPC * WN / 2) void k_linear_tile(con
         step(k, f0, f1);
         step(k + 1, f1, f0);
     }
-    if constexpr (BK == 64)                 // (K is a multiple of 64: an even number of steps of 32)
+    if constexpr (BK >= 64) {               // (K is a multiple of 64: an even number of steps of 32)
         if (nk & 1) step(nk - 1, f0, f1);
+        if (rest && kg == 0) mma(nk & 1 ? f1 : f0);          // the half step, read under the last whole one
+    }
     wait_vm<0>();
 
     // ---- epilogue: 32 rows of the wave's tile at a time through its part of the
     // LDS, then 8 consecutive outputs a lane
     __syncthreads();                                          // every wave has read its last fragments, every load has landed
-    unsigned char* ep = smem + wv * 32 * G::EROW;
+    if constexpr (KG > 1) {                                   // the k groups' sums meet in the first
+        f32x4_t* xch = reinterpret_cast<f32x4_t*>(smem + G::EPI);
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < IT; i++)
+#pragma unroll
+                for (int j = 0; j < JT; j++) xch[((wv - 2 * WN) * IT * JT + i * JT + j) * WAVE + l] = acc[i][j];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int k2 = 0; k2 < KG - 1; k2++)
+#pragma unroll
+            for (int i = 0; i < IT; i++)
+#pragma unroll
+                for (int j = 0; j < JT; j++) acc[i][j] += xch[((k2 * 2 * WN + w4) * IT * JT + i * JT + j) * WAVE + l];
+    }
+    unsigned char* ep = smem + w4 * 32 * G::EROW;
     constexpr int LPR = G::WNC / 8, RPP = WAVE / LPR, NP = 32 / RPP;     // lanes per row, rows per pass, passes
     const int er = l / LPR, ec = l % LPR * 8, n = n0 + wn * G::WNC + ec;
     f32x4_t b[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -415,30 +461,45 @@ hipError_t launch_rows_k(const LinearArgs& a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-template <int BT, int BN, int BK, int ST, int WN, int BPC, int OB>
+template <int BT, int BN, int BK, int ST, int WN, int KG, int BPC, int OB>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
-    auto kern = k_linear_tile<BT, BN, BK, ST, WN, OB, BPC>;
+    auto kern = k_linear_tile<BT, BN, BK, ST, WN, KG, OB, BPC>;
     static LdsLimit lim;
-    constexpr int lds = TileGeo<BT, BN, BK, ST, WN>::LDS;
+    constexpr int lds = TileGeo<BT, BN, BK, ST, WN, KG>::LDS;
     hipError_t e = lim.ensure((const void*)kern, lds);
     if (e != hipSuccess) return e;
     const int tt = (a.T + BT - 1) / BT, tn = (a.N + BN - 1) / BN, per = (tt * tn + 7) / 8;
-    hipLaunchKernelGGL(kern, dim3(per * 8), dim3(2 * WN * WAVE), lds, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual,
+    hipLaunchKernelGGL(kern, dim3(per * 8), dim3(2 * WN * KG * WAVE), lds, st, a.x, a.x_stride, a.w, a.bias, a.act, a.residual,
                        a.T, a.N, a.K, tt, tn, a.out);
     return hipGetLastError();
 }
 
 template <int OB>
 hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
-    if (a.T <= ROWS_MAX_T) {
+    // Few rows: 17 to 32 rows cost the rows kernel a second product per weight, which
+    // narrow weights hide (24 x 2048 x 8192: 19.5 us, tiles 23) and wide ones do not (24 x 5120 x 8192:
+    // 38, tiles 24); from 33 rows on tiles are as good throughout.
+    if (a.T <= 16 || (a.T <= ROWS_MAX_T && a.N <= 2048)) {
         if (a.K <= 1024 || a.T > 16) return launch_rows_k<1, OB>(a, st);
         if (a.K <= 2048) return launch_rows_k<2, OB>(a, st);
         return launch_rows_k<4, OB>(a, st);
     }
-    auto tiles = [&](int bt, int bn) { return (int64_t)((a.T + bt - 1) / bt) * ((a.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= 192) return launch_tile<256, 256, 32, 4, 4, 1, OB>(a, st);
-    if (tiles(128, 128) >= 192) return launch_tile<128, 128, 32, 4, 2, 2, OB>(a, st);
-    return launch_tile<64, 64, 64, 8, 2, 1, OB>(a, st);
+    auto tiles = [&](int b) { return (int64_t)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };
+    auto rounds = [&](int b) { return (tiles(b) + 255) / 256; };             // tiles a CU is given
+    // Which tile: a CU works off its tiles one after the other or two side by side,
+    // and the time of a round is that of its slowest CU, so each size's time is that of
+    // a round times the rounds, in units that fit the times at K = 2048 (us: 64-square 9
+    // for a lone tile, 7 per tile and CU after that, 128-square 23 and 18, 256-square
+    // 44).  Both sides: 1600 x 5120 x 2048, 256-square 46 us, 128 57, 64 57; 3200 x 5120 x 512
+    // (260 of the largest, a second round for four of them) 36, 28, 38; 3200 x 2048 x 2048 45, 37, 48;
+    // 800 x 2048 x 8192 137, 74, 48.  Over 90 sizes up to 8192 rows the choice was the best
+    // one or within 8 percent of it, but for 4000 x 768 x 1024 (15.4 against 12.3).
+    const int64_t c64 = rounds(64) == 1 ? 9 : rounds(64) * 7, c128 = rounds(128) == 1 ? 23 : rounds(128) * 18,
+                  c256 = rounds(256) * 44;
+    if (c256 < c128 && c256 < c64) return launch_tile<256, 256, 32, 4, 4, 1, 1, OB>(a, st);
+    if (c128 < c64) return launch_tile<128, 128, 32, 4, 2, 1, 2, OB>(a, st);
+    if (tiles(64) <= 256 && a.K >= 2048) return launch_tile<64, 64, 128, 4, 2, 2, 1, OB>(a, st);
+    return launch_tile<64, 64, 64, 4, 2, 1, 2, OB>(a, st);
 }
 
 }  // namespace

@@ -396,6 +396,11 @@ LINEARS = [
     (1700, 1800, 320, "gelu", True, True, BF),       # 128-square tiles
     (3900, 3400, 192, None, False, True, BF),        # 256-square tiles
     (3841, 3336, 64, "gelu_tanh", True, False, torch.float32),
+    (40, 264, 2112, "silu", True, True, torch.float32),     # k in two halves a block, the last step half full
+    (33, 72, 2048, None, False, False, BF),
+    (130, 200, 4160, "gelu", True, True, BF),
+    (29, 2056, 2176, None, True, False, torch.float32),     # tiles below 33 rows
+    (20, 2560, 128, "relu", False, True, BF),
 ]
 
 
