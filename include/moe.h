@@ -424,7 +424,8 @@ moe_status moe_qk_norm_rope(const void* qkv, int32_t x_dtype, int64_t qkv_stride
  *               behind q_offsets[S] are left as they were.
  * Long caches are split over the GPU's compute units and joined by a second
  * kernel, in a fixed order: the result does not vary from run to run.  scale,
- * softcap, and for moe_qk_norm_rope eps >= 0 and rope_scale, must be finite.
+ * softcap, scale / softcap and their products with log2 e must be finite, and for
+ * moe_qk_norm_rope eps >= 0 and rope_scale.
  * Unsupported: q_dtype other than MOE_BF16; S > 4096; n_heads not a multiple of
  * n_kv_heads, or n_heads / n_kv_heads > 64; q_stride not a multiple of 8;
  * n_heads head_dim / 64 > 65535; W * page_size > 2^30; (T n_heads / 16 + S n_kv_heads) (W page_size / 32 + 9)

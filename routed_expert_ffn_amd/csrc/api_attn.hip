@@ -94,6 +94,10 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
     if (T < 0 || n_heads <= 0 || W <= 0 || S_ <= 0 || window < 0 || !(softcap >= 0.0f) || !std::isfinite(softcap) ||
         !std::isfinite(scale))
         return MOE_ERR_INVALID_ARG;
+    // the kernel's own factors, in units of log2, must be finite too
+    const float log2e = 1.44269504088896341f;
+    if (!std::isfinite(scale * log2e) || !std::isfinite(softcap * log2e) || (softcap > 0.0f && !std::isfinite(scale / softcap)))
+        return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_F32 && q_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     KvView kv;
     const moe_status chk = cache_view(cache, &kv);
@@ -101,7 +105,8 @@ moe_status moe_paged_attn(const void* q, int32_t q_dtype, int64_t q_stride, int3
     if (!page_table || !q_offsets || !kv_len || (T > 0 && (!q || !out))) return MOE_ERR_INVALID_ARG;
     if (q_stride < (int64_t)n_heads * kv.head_dim || (int64_t)T * n_heads > (int64_t)1 << 30) return MOE_ERR_INVALID_ARG;
     if (q_dtype != MOE_BF16 || S_ > MAX_REQUESTS || n_heads % kv.n_kv_heads != 0 ||
-        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)n_heads * kv.head_dim > 64 * 65535 || (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
+        n_heads / kv.n_kv_heads > MAX_GROUP || q_stride % 8 != 0 || (int64_t)n_heads * kv.head_dim > 64 * 65535 ||
+        (int64_t)W * (1 << kv.page_shift) > ((int64_t)1 << 30))
         return MOE_ERR_UNSUPPORTED;
     // the steps of all units (16 rows of a key-value head, 32 positions at least) are counted in int32
     if ((((int64_t)T * n_heads + 15) / 16 + (int64_t)S_ * kv.n_kv_heads) * (((int64_t)W << kv.page_shift) / 32 + 9) > INT32_MAX)

@@ -267,9 +267,11 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
         rq.n = uniform(rq.n);
         rq.first = uniform(rq.first);
         rq.len = uniform(rq.len);
+        rq.units = uniform(rq.units);
         rq.steps = uniform(rq.steps);
         // the piece: steps [st0, st1) of unit (row group, head)
         const int unit = uniform((int)((uint32_t)(at - s_base) / (uint32_t)rq.steps));
+        if ((uint32_t)unit >= (uint32_t)rq.units) return;    // (offsets that do not ascend, their steps past int32: no row is read)
         const int st0 = at - s_base - unit * rq.steps;
         if (a.whole && st0 > 0) {           // the share before has it
             at += rq.steps - st0;
@@ -819,7 +821,7 @@ __global__ __launch_bounds__(WPR == 1 ? AT_THREADS : WPR * WAVE) void k_attn_joi
         return q + ((int64_t)(q + 1) * share <= u ? 1 : 0) - ((int64_t)q * share > u ? 1 : 0);
     };
     const int b0 = share_of(u0), np = share_of(u0 + rq.steps - 1) - b0 + 1;
-    if (np <= 1) return;
+    if (np <= 1 || b0 < 0 || b0 + np > a.shares) return;     // (past the shares only with offsets that do not ascend)
     const int first_odd = u0 == b0 * share ? 0 : 1;
     const int e = l % TC, gr = (WPR == 1 ? 0 : w * GW) + l / TC;
     float M = -__builtin_inff(), L = 0.f;

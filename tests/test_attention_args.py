@@ -90,6 +90,7 @@ def test_paged_attn_refuses(L):
     assert call(cap=-1.0) == INVALID and call(cap=float("nan")) == INVALID and call(qd=9) == INVALID
     for bad in (float("nan"), float("inf")):
         assert call(cap=bad) == INVALID and call(sc=bad) == INVALID
+    assert call(cap=1e-42) == INVALID and call(cap=3e38) == INVALID and call(sc=3e38) == INVALID   # scale / cap, x log2 e
     assert call(st=8) == INVALID and call(T=1 << 27, h=16, c=cache()) == INVALID
     assert call(qd=moe.F32) == UNSUPPORTED and call(S=4097) == UNSUPPORTED and call(h=15) == UNSUPPORTED
     assert call(h=130, st=130 * 128) == UNSUPPORTED                        # 65 query heads per key-value head
