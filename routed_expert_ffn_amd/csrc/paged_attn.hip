@@ -29,81 +29,13 @@
 // the order of the shares.
 //
 // Bound by HBM at few rows: each cached byte is used for 16 MT rows at a time.
-#include "attn.h"
-#include "common.h"
+#include "attn_split.h"
 #include "device.h"
-#include "stream.h"
 
 namespace {
 
 constexpr int NW = 4;                       // waves per block
-constexpr int AT_THREADS = NW * WAVE;
-constexpr float LOG2E = 1.44269504088896341f;
-
-typedef uint32_t u32x2_a __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_a __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2_a __attribute__((ext_vector_type(2)));
-typedef short s16x4_a __attribute__((ext_vector_type(4)));
-
-MOE_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-MOE_DEV uint32_t pk_bf16(float lo, float hi) {
-    const bf16x2_a v = {(__bf16)lo, (__bf16)hi};
-    return __builtin_bit_cast(uint32_t, v);
-}
-// two e4m3 of word w (its low or high half) -> packed bf16 (exact)
-template <bool HI>
-MOE_DEV uint32_t fp8x2_bf16(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
-}
-
-// What a piece costs besides its own positions (its q rows, first loads and
-// join), in positions: short requests would otherwise pile up in few shares.
-constexpr int PIECE_COST = 128;
-
-struct AttnArgs {
-    const uint16_t* q;
-    int64_t q_stride;
-    int T, n_heads;
-    KvView kv;
-    const int32_t* table;
-    int W;
-    const int32_t* q_offsets;
-    const int32_t* kv_len;
-    int S;
-    float scale, softcap;
-    int window;
-    uint16_t* out;
-    int G;                                  // query heads per key-value head
-    int G16;                                // ceil(2^16 / G): x / G = x G16 >> 16 for x < 1024
-    int whole;                              // no unit is split: each goes to the share that its first step lies in
-    int shares;                             // blocks of the attention launch
-    int* share;                             // [1] steps per share, written by block 0 for the join
-    int* base;                              // [S] first step of each request
-    float* part;                            // [2 shares][rows][D] unnormalised sums
-    float2* ml;                             // [2 shares][rows] (maximum, sum)
-};
-
-// What a block needs of a request: its row range, positions and units.
-struct Request {
-    int row0, n, first;                     // first batch row, rows, position of its first row
-    int len;                                // positions that the table can hold
-    int units;                              // row groups * key-value heads
-    int steps;                              // cost of each of its units, in steps
-};
-template <int RB, int STEP>
-MOE_DEV Request request_of(const AttnArgs& a, int s) {
-    Request r;
-    const int b = min(max(a.q_offsets[s], 0), a.T), e = min(max(a.q_offsets[s + 1], 0), a.T);
-    const int L = min(max(a.kv_len[s], 0), 1 << 30);
-    r.row0 = b;
-    r.n = max(e - b, 0);
-    r.first = L - r.n;
-    r.len = (int)min((int64_t)L, (int64_t)a.W << a.kv.page_shift);
-    const int lo = a.window > 0 ? max(r.first - a.window + 1, 0) : 0;
-    r.units = (int)(((uint32_t)(r.n * a.G) + RB - 1) / RB) * a.kv.n_kv_heads;      // (T * n_heads fits int32)
-    r.steps = (max(r.len - lo, 0) + STEP - 1) / STEP + PIECE_COST / STEP;
-    return r;
-}
+static_assert(NW * WAVE == AT_THREADS);
 
 // One wave's NSUB sub-tiles of 16 positions.
 template <int D, int F8, int NSUB, int DS>
@@ -129,18 +61,6 @@ template <int AUX>
 MOE_DEV u32x2_a buf64(rsrc_t r, int off) { return __builtin_bit_cast(u32x2_a, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, AUX)); }
 template <int AUX>
 MOE_DEV uint32_t buf32(rsrc_t r, int off) { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, AUX); }
-
-// the page table through the scalar cache (nothing writes it while the kernel runs)
-typedef const __attribute__((address_space(4))) int32_t* table_ptr;
-
-// First element of four consecutive results c of a row as the second product
-// leaves them, (h, e, 4 g + i): elements 16 E h + E (4 g + i) + e, i = 0 .. 3.
-template <int D>
-MOE_DEV int dim_of(int c) {
-    constexpr int E = D == 64 ? 4 : 8;
-    const int g = c & 3, e = (c >> 2) % E, h = (c >> 2) / E;
-    return 16 * E * h + 4 * E * g + e;
-}
 
 // blocks per CU, by registers
 constexpr int blocks_per_cu(int D, int MT) { return MT == 1 || D == 64 || (D == 128 && MT == 2) || (D == 256 && MT == 2) ? 2 : 1; }
@@ -191,7 +111,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     Request mine;
     int my_base = 0, total;
     if (lanes) {
-        mine = request_of<RB, STEP>(a, min(l, a.S - 1));
+        mine = request_of<RB, STEP, false>(a, min(l, a.S - 1));
         if (l >= a.S) mine.units = 0;
         const int c = mine.units * mine.steps, incl = wave_incl_scan(c);
         total = __builtin_amdgcn_readlane(incl, WAVE - 1);
@@ -203,7 +123,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
             const int s = s0 + tid;
             int c = 0;
             if (s < a.S) {
-                const Request r = request_of<RB, STEP>(a, s);
+                const Request r = request_of<RB, STEP, false>(a, s);
                 c = r.units * r.steps;
             }
             const int incl = wave_incl_scan(c);
@@ -256,7 +176,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
                 else hi = mid;
             }
             s = __builtin_amdgcn_readfirstlane(s);
-            rq = request_of<RB, STEP>(a, s);
+            rq = request_of<RB, STEP, false>(a, s);
             s_base = base[s];
         }
         // (the same in every lane, and kept in scalar registers: buffer descriptors
@@ -780,107 +700,7 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     }
 }
 
-// The request that batch row t lies in, searched by a wave: 64 offsets at a time.
-MOE_DEV int request_with(const AttnArgs& a, int t) {
-    const int l = lane_id();
-    int s = 0, stride = 1;
-    while (stride * WAVE < a.S) stride *= WAVE;
-    for (; stride >= 1; stride /= WAVE) {
-        const int i = s + l * stride;
-        s += max(__popcll(__ballot(i < a.S && a.q_offsets[min(i, a.S - 1)] <= t)) - 1, 0) * stride;
-    }
-    return uniform(s);
-}
-
-// out = sum_c 2^{m_c - M} acc_c / sum_c 2^{m_c - M} sum_c over the shares c that a
-// unit lies in.  WPR waves per (batch row, head, CH elements): CH / 4 lanes of 4
-// elements each, the shares dealt to the groups of them in all WPR waves, joined
-// across lanes and then through LDS in order.  Few rows take CH 64 and 16 or 4
-// waves (a unit in hundreds of shares; one token over 262,144 positions: 11 us
-// with 4 waves, 6 with 16), many rows one wave each (most of them in one share,
-// with nothing to do).
-template <int D, int RB, int STEP, int CH, int WPR>
-__global__ __launch_bounds__(WPR == 1 ? AT_THREADS : WPR * WAVE) void k_attn_join(const AttnArgs a) {
-    constexpr int NC = D / CH, TC = CH / 4, GW = WAVE / TC, NG = GW * WPR;
-    constexpr int U = 4;                   // shares in flight per thread
-    __shared__ float2 gml[WPR];
-    __shared__ f32x4_t go[WPR][TC];
-    const int l = lane_id(), w = uniform(threadIdx.x / WAVE);
-    const int t = blockIdx.x, y = WPR == 1 ? blockIdx.y * NW + w : blockIdx.y, hq = y / NC, c0 = y % NC * TC;
-    const int share = a.share[0];
-    const int s = request_with(a, t);
-    const Request rq = request_of<RB, STEP>(a, s);
-    if (hq >= a.n_heads || t < rq.row0 || t >= rq.row0 + rq.n) return;
-    const int nkv = a.kv.n_kv_heads, G = a.G;
-    const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
-    const int grp = row / RB, rr = row - grp * RB;
-    const int u0 = a.base[s] + (grp * nkv + head) * rq.steps;    // the unit's first step
-    // (at most shares - 1 <= 511: the fp32 quotient is off by one at most)
-    auto share_of = [&](int u) {
-        const int q = (int)((float)u * __builtin_amdgcn_rcpf((float)share));
-        return q + ((int64_t)(q + 1) * share <= u ? 1 : 0) - ((int64_t)q * share > u ? 1 : 0);
-    };
-    const int b0 = share_of(u0), np = share_of(u0 + rq.steps - 1) - b0 + 1;
-    if (np <= 1 || b0 < 0 || b0 + np > a.shares) return;     // (past the shares only with offsets that do not ascend)
-    const int first_odd = u0 == b0 * share ? 0 : 1;
-    const int e = l % TC, gr = (WPR == 1 ? 0 : w * GW) + l / TC;
-    float M = -__builtin_inff(), L = 0.f;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](float m2, float l2, f32x4_t v2) __attribute__((always_inline)) {
-        const float mn = fmaxf(M, m2), base = mn == -__builtin_inff() ? 0.f : mn;
-        const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(m2 - base);
-        L = L * f0 + l2 * f1;
-        o = o * f0 + v2 * f1;
-        M = mn;
-    };
-    for (int p0 = gr; p0 < np; p0 += NG * U) {
-        float2 x[U];
-        f32x4_t v[U];
-#pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int p = min(p0 + i * NG, np - 1);
-            const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
-            x[i] = a.ml[at];
-            v[i] = *reinterpret_cast<const f32x4_t*>(a.part + at * D + (c0 + e) * 4);
-        }
-#pragma unroll
-        for (int i = 0; i < U; i++) {
-            if (p0 + i * NG >= np) break;
-            add(x[i].x, x[i].y, v[i]);
-        }
-    }
-    // the wave's groups: every lane ends with the sum over them, taken in the
-    // same order (its own pair's lower group first)
-#pragma unroll
-    for (int d = TC; d < WAVE; d <<= 1) {
-        const bool low = (l & d) == 0;
-        const float m2 = wave_xor(M, d), l2 = wave_xor(L, d);
-        f32x4_t v2;
-#pragma unroll
-        for (int i = 0; i < 4; i++) v2[i] = wave_xor(o[i], d);
-        const float m1 = M, l1 = L;
-        const f32x4_t v1 = o;
-        M = low ? m1 : m2; L = low ? l1 : l2; o = low ? v1 : v2;
-        add(low ? m2 : m1, low ? l2 : l1, low ? v2 : v1);
-    }
-    if constexpr (WPR > 1) {
-        if (l < TC) go[w][l] = o;
-        if (l == 0) gml[w] = make_float2(M, L);
-        __syncthreads();
-        if (threadIdx.x >= TC) return;
-        M = -__builtin_inff();
-        L = 0.f;
-        o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = 0; i < WPR; i++) add(gml[i].x, gml[i].y, go[i][e]);
-    } else if (l >= TC) {
-        return;
-    }
-    const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);
-    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c0 + e);
-#pragma unroll
-    for (int i = 0; i < 4; i++) dst[(D == 64 ? 4 : 8) * i] = (uint16_t)pk_bf16(o[i] * inv, 0.f);
-}
+constexpr int PROMPT_MIN_ROWS = 64;
 
 // Row tiles per unit: as many as a request has rows on average, so that its
 // cache is read once; more than 64 rows (48 at head_dim 256, where the
@@ -892,14 +712,19 @@ int row_tiles(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
     return mt < 1 ? 1 : mt;
 }
 
+// Many rows per request: prompt_attn.hip's kernel.
+bool many_rows(int T, int n_heads, int n_kv_heads, int S) { return (int64_t)T * (n_heads / n_kv_heads) > (int64_t)PROMPT_MIN_ROWS * S; }
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct AttnWs {
     size_t ml, part, total;
 };
 AttnWs attn_ws(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
-    const int mt = row_tiles(T, n_heads, n_kv_heads, head_dim, S), rb = 16 * mt;
-    const size_t parts = 2 * (size_t)shares_of(head_dim, mt);
+    const int mt = row_tiles(T, n_heads, n_kv_heads, head_dim, S);
+    const PromptShape ps = prompt_attn_shape();
+    const bool many = many_rows(T, n_heads, n_kv_heads, S);
+    const size_t rb = many ? ps.rows : 16 * mt, parts = 2 * (size_t)(many ? ps.shares : shares_of(head_dim, mt));
     AttnWs w;
     w.ml = up256(((size_t)S + 1) * sizeof(int));
     w.part = w.ml + up256(parts * rb * sizeof(float2));
@@ -923,9 +748,9 @@ hipError_t launch_attn(AttnArgs a, hipStream_t st) {
     if (a.whole) return hipGetLastError();
     const int64_t chunks = (int64_t)a.T * a.n_heads * (D / 64);
     auto launch_join = [&](auto kern, dim3 grid, int threads) { hipLaunchKernelGGL(kern, grid, dim3(threads), 0, st, a); };
-    if (chunks <= 128) launch_join(k_attn_join<D, 16 * MT, SH::STEP, 64, 16>, dim3(a.T, a.n_heads * (D / 64)), 16 * WAVE);
-    else if (chunks <= 1024) launch_join(k_attn_join<D, 16 * MT, SH::STEP, 64, 4>, dim3(a.T, a.n_heads * (D / 64)), 4 * WAVE);
-    else launch_join(k_attn_join<D, 16 * MT, SH::STEP, D, 1>, dim3(a.T, (a.n_heads + NW - 1) / NW), AT_THREADS);
+    if (chunks <= 128) launch_join(k_attn_join<D, 16 * MT, SH::STEP, false, 64, 16>, dim3(a.T, a.n_heads * (D / 64)), 16 * WAVE);
+    else if (chunks <= 1024) launch_join(k_attn_join<D, 16 * MT, SH::STEP, false, 64, 4>, dim3(a.T, a.n_heads * (D / 64)), 4 * WAVE);
+    else launch_join(k_attn_join<D, 16 * MT, SH::STEP, false, D, 1>, dim3(a.T, (a.n_heads + NW - 1) / NW), AT_THREADS);
     return hipGetLastError();
 }
 
@@ -964,6 +789,7 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     a.share = (int*)wb; a.base = (int*)wb + 1;
     a.G = n_heads / cache.n_kv_heads; a.G16 = (65536 + a.G - 1) / a.G;
     a.ml = (float2*)(wb + L.ml); a.part = (float*)(wb + L.part);
+    if (many_rows(T, n_heads, cache.n_kv_heads, S)) return launch_prompt_attn(a, st);
     const int mt = row_tiles(T, n_heads, cache.n_kv_heads, cache.head_dim, S);
     const bool f8 = cache.k_scale != nullptr;
     switch (cache.head_dim) {

@@ -282,6 +282,76 @@ def test_paged_attention_every_shape(D, fp8, new):
     check_attn(st, run_attn(st, softcap=5.0, window=37), softcap=5.0, window=37)
 
 
+MANY_ROWS = [
+    # whole prompts and chunks: more than 64 rows (query token x head) per key-value head and request
+    ([300, 200], [300, 150], 8, 2, 128, 16, False, 0, 0.0),
+    ([700, 5, 410], [400, 1, 300], 4, 1, 256, 16, False, 0, 0.0),
+    ([700, 5, 410], [400, 0, 300], 4, 1, 256, 32, True, 0, 30.0),
+    ([1200, 300], [333, 77], 4, 2, 64, 16, False, 100, 0.0),
+    ([1200, 300, 64], [333, 77, 64], 4, 2, 64, 64, True, 100, 20.0),
+    ([900], [129], 3, 3, 128, 16, True, 0, 0.0),                     # a row per token
+    ([200, 100], [40, 30], 64, 1, 64, 32, False, 0, 0.0),            # the largest group
+    ([3000], [70], 12, 2, 128, 1024, False, 0, 0.0),                 # a group of 6 across tiles, units in many shares
+    ([5000], [200], 2, 1, 256, 16, False, 1, 0.0),                   # a window of one
+    ([257] * 5, [257] * 5, 2, 2, 64, 16, False, 0, 0.0),
+    ([256, 250], [256, 250], 4, 4, 256, 256, True, 40, 0.0),         # 512 positions at most: units stay whole
+    ([(i * 37) % 150 + 60 for i in range(520)], [60] * 520, 2, 1, 64, 16, False, 0, 0.0),     # more requests than threads
+]
+
+
+@pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: "-".join(map(str, c[2:])).replace(" ", ""))
+def test_paged_attention_many_rows(case):
+    lens, new, Hq, Hkv, D, page, fp8, window, cap = case
+    st = attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=sum(lens), pad=3)
+    check_attn(st, run_attn(st, softcap=cap, window=window), softcap=cap, window=window)
+
+
+@pytest.mark.parametrize("new", [80, 150])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_paged_attention_many_rows_every_shape(D, fp8, new):
+    st = attn_state([new + 550, new, new + 7], [new] * 3, 8, 2, D, 32, fp8, seed=new, pad=1)
+    a = run_attn(st)
+    check_attn(st, a)
+    assert torch.equal(a.view(torch.int16), run_attn(st).view(torch.int16))
+    check_attn(st, run_attn(st, softcap=5.0, window=37), softcap=5.0, window=37)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 256])
+def test_paged_attention_many_rows_that_see_nothing(D, fp8):
+    st = attn_state([0, 2, 400, 600], [90, 80, 200, 300], 4, 2, D, 16, fp8, seed=3)
+    table = st["table"].clone()
+    table[2] = -1                                    # request 2 has no page
+    table[3, 9] = st["cache"].num_pages              # request 3 lacks positions 144..159 and 368..399
+    table[3, 23:25] = -7
+    got = run_attn(st, table=table)
+    check_attn(st, got, table=table)
+    assert bool((got[:168] == 0).all()) and bool((got[170:370] == 0).all())
+
+
+@pytest.mark.parametrize("D,fp8", [(64, False), (128, True), (256, False)])
+def test_paged_attention_many_rows_unseen_infinities_do_not_reach_a_row(D, fp8):
+    st = attn_state([700], [300], 4, 2, D, 16, fp8, seed=5)
+    at = 650                                          # rows 0 .. 249 do not see it
+    page, off = int(st["table"][0, at // 16]), at % 16
+    if fp8:
+        st["cache"].v.view(torch.uint8)[page, :, off, 3] = 0x7F
+    else:
+        st["cache"].v[page, :, off, 3] = math.inf
+    st["v"][page, :, off, 3] = math.nan if fp8 else math.inf
+    got = run_attn(st)
+    want, mass, reach = ref.attention(st["q"], st["k"], st["v"], st["table"], st["offs"], st["lens"], 16, D ** -0.5,
+                                      0.0, 0)
+    bound = ref.attention_bound(want, mass, reach, D, 700)
+    n = at - 400
+    assert bool(((got[:n].double() - want[:n]).abs() <= bound[:n]).all())
+    tail = got[n:].double()
+    assert bool(torch.isnan(tail[:, :, 3]).all()) if fp8 else bool((tail[:, :, 3] == math.inf).all())
+    rest = [d for d in range(D) if d != 3]
+    assert bool(((tail - want[n:]).abs() <= bound[n:])[:, :, rest].all())
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_paged_attention_rows_that_see_nothing(fp8):
     # no cached position at all; more rows than positions; pages outside the cache
