@@ -700,8 +700,6 @@ __global__ __launch_bounds__(AT_THREADS, (blocks_per_cu(D, MT))) void k_paged_at
     }
 }
 
-constexpr int PROMPT_MIN_ROWS = 64;
-
 // Row tiles per unit: as many as a request has rows on average, so that its
 // cache is read once; more than 64 rows (48 at head_dim 256, where the
 // accumulators take MT x 64 registers) go over it again.
@@ -712,8 +710,21 @@ int row_tiles(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
     return mt < 1 ? 1 : mt;
 }
 
-// Many rows per request: prompt_attn.hip's kernel.
-bool many_rows(int T, int n_heads, int n_kv_heads, int S) { return (int64_t)T * (n_heads / n_kv_heads) > (int64_t)PROMPT_MIN_ROWS * S; }
+// Many rows per request: prompt_attn.hip's kernel reads the cache once for 256
+// rows, where this one goes over it again for every 64, but its blocks take longer to
+// fill and leave more to join.  It is taken from 2^25 scores on (rows x positions of
+// the table or window; the requests' own lengths are on the device), if the
+// requests have more than 128 rows on average.  Both sides, this one's time first, on
+// requests of r rows x positions, 2 key-value heads: D 128, 8 of 256 x 16,384 115 us against 82,
+// of 1024 x 2048 63 against 58 and below the bound 8 of 512 x 2048 49 against 53; D 256, 1024 x 16,384 126
+// against 113, 8 of 512 x 2048 79 against 90; D 64, 1024 x 16,384 47 against 42, 8 of 512 x 2048 37
+// against 43; at 128 rows, D 256, 8 x 16,384 145 against 170.
+bool many_rows(int T, int n_heads, int n_kv_heads, int S) { return (int64_t)T * (n_heads / n_kv_heads) > (int64_t)128 * S; }
+bool take_prompt(const AttnArgs& a) {
+    const int64_t table = (int64_t)a.W << a.kv.page_shift, seen = (int64_t)a.window + a.T / a.S;
+    return many_rows(a.T, a.n_heads, a.kv.n_kv_heads, a.S) &&
+           (int64_t)a.T * a.n_heads * (a.window > 0 && seen < table ? seen : table) >= 1 << 25;
+}
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -723,12 +734,12 @@ struct AttnWs {
 AttnWs attn_ws(int T, int n_heads, int n_kv_heads, int head_dim, int S) {
     const int mt = row_tiles(T, n_heads, n_kv_heads, head_dim, S);
     const PromptShape ps = prompt_attn_shape();
-    const bool many = many_rows(T, n_heads, n_kv_heads, S);
-    const size_t rb = many ? ps.rows : 16 * mt, parts = 2 * (size_t)(many ? ps.shares : shares_of(head_dim, mt));
+    const size_t few = (size_t)shares_of(head_dim, mt) * 16 * mt, many = (size_t)ps.shares * ps.rows;
+    const size_t rows = 2 * (many_rows(T, n_heads, n_kv_heads, S) && many > few ? many : few);
     AttnWs w;
     w.ml = up256(((size_t)S + 1) * sizeof(int));
-    w.part = w.ml + up256(parts * rb * sizeof(float2));
-    w.total = w.part + up256(parts * rb * head_dim * sizeof(float));
+    w.part = w.ml + up256(rows * sizeof(float2));
+    w.total = w.part + up256(rows * head_dim * sizeof(float));
     return w;
 }
 
@@ -789,7 +800,7 @@ hipError_t launch_paged_attn(const uint16_t* q, int64_t q_stride, int T, int n_h
     a.share = (int*)wb; a.base = (int*)wb + 1;
     a.G = n_heads / cache.n_kv_heads; a.G16 = (65536 + a.G - 1) / a.G;
     a.ml = (float2*)(wb + L.ml); a.part = (float*)(wb + L.part);
-    if (many_rows(T, n_heads, cache.n_kv_heads, S)) return launch_prompt_attn(a, st);
+    if (take_prompt(a)) return launch_prompt_attn(a, st);
     const int mt = row_tiles(T, n_heads, cache.n_kv_heads, cache.head_dim, S);
     const bool f8 = cache.k_scale != nullptr;
     switch (cache.head_dim) {

@@ -216,7 +216,8 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
         for (int k = 0; k < SG::ST - 1; k++)
             if (k < n) ok[k] = issue(k);
         bf16x8_t qf[PMT][D / 32];
-        int vlo[PMT], vhi[PMT];
+        int vlo[PMT];
+        uint32_t vn[PMT];                   // this lane's rows see [vlo, vlo + vn)
 #pragma unroll
         for (int mt = 0; mt < PMT; mt++) {
             const int x = x0 + mt * 16 + r16, xs = r_in + min(x, nrows - 1), i = (xs * a.G16) >> 16;   // (rows past the unit's repeat its last, unused)
@@ -225,8 +226,8 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
             for (int k = 0; k < D / 32; k++)
                 qf[mt][k] = *reinterpret_cast<const bf16x8_t*>(q + (F8 ? 16 * (4 * (k >> 1) + g4) + 8 * (k & 1) : 32 * k + 8 * g4));
             const int p = rq.first + i0 + i;
-            vhi[mt] = x < nrows ? min(p, t_hi - 1) : -1;
             vlo[mt] = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+            vn[mt] = x < nrows ? (uint32_t)max(min(p + 1, t_hi) - vlo[mt], 0) : 0u;
         }
         f32x4_t acc[PMT][NH][E], sum[PMT];
         float m[PMT];
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
 #pragma unroll
                 for (int e = 0; e < E; e++) acc[mt][h][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
-        bool strange = false;               // infinite or NaN values in a tile seen in part
+        uint32_t strange = 0;               // not 0: infinite or NaN values in a tile seen in part
 
         // 32 positions from t0, their sub-tiles at `st`; ok2: which of the two have a page
         auto half = [&](const unsigned char* st, const unsigned char* sc_at, int t0, int ok2) __attribute__((always_inline)) {
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
 #pragma unroll
                 for (int sb = 0; sb < 2; sb++) sc[mt][sb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < D / 32; k++)
+            for (int k = 0; k < D / 32; k++) {
 #pragma unroll
                 for (int sb = 0; sb < 2; sb++) {
                     bf16x8_t kf;
@@ -264,6 +265,7 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
 #pragma unroll
                     for (int mt = 0; mt < PMT; mt++) sc[mt][sb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[mt][k], sc[mt][sb], 0, 0, 0);
                 }
+            }
             f32x4_t vs[2];
 #pragma unroll
             for (int sb = 0; sb < 2; sb++) {
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
                     if (a.softcap > 0.f)
 #pragma unroll
                         for (int i = 0; i < 4; i++)
-                            sc[mt][sb][i] = capk * (1.f - 2.f * __builtin_amdgcn_rcpf(exp2f(sc[mt][sb][i] * (2.f * LOG2E)) + 1.f));
+                            sc[mt][sb][i] = capk * (1.f - 2.f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(sc[mt][sb][i] * (2.f * LOG2E)) + 1.f));
                 }
             }
             if (!whole) {
@@ -287,8 +289,8 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
                 for (int mt = 0; mt < PMT; mt++)
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const int pos = t0 + 16 * (j >> 2) + 4 * g4 + (j & 3);
-                        if (!((ok2 >> (j >> 2)) & 1) || pos < vlo[mt] || pos > vhi[mt]) sc[mt][j >> 2][j & 3] = -__builtin_inff();
+                        const uint32_t at2 = (uint32_t)(t0 + 16 * (j >> 2) + 4 * g4 + (j & 3) - vlo[mt]);
+                        if (at2 >= ((ok2 >> (j >> 2)) & 1 ? vn[mt] : 0u)) sc[mt][j >> 2][j & 3] = -__builtin_inff();
                     }
             }
             // ---- softmax: the exponentials' base follows a row's maximum only when
@@ -372,22 +374,18 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
                 // ones for now (0 * inf is NaN: they must not meet the zero probability
                 // of a row that does not see them); add_strange() adds those
                 if (!whole) {
+                    const uint32_t span = (uint32_t)max(min(w_hi + 1, t_hi) - w_lo, 0);
 #pragma unroll
                     for (int j = 0; j < 8; j++) {
-                        const int pos = t0 + 16 * (j >> 2) + 4 * g4 + (j & 3);
-                        const bool in = ((ok2 >> (j >> 2)) & 1) && pos >= w_lo && pos <= w_hi && pos < t_hi;
+                        const uint32_t at2 = (uint32_t)(t0 + 16 * (j >> 2) + 4 * g4 + (j & 3) - w_lo);
+                        const uint32_t in = at2 < ((ok2 >> (j >> 2)) & 1 ? span : 0u) ? 0xFFFFFFFFu : 0u;
 #pragma unroll
                         for (int q = 0; q < EW; q++) {
-                            const uint32_t y = in ? v[j][q] : 0u;
-                            uint32_t keep = 0;
-                            if constexpr (F8) {
-#pragma unroll
-                                for (int c = 0; c < 4; c++) keep |= ((y >> (8 * c)) & 0x7Fu) == 0x7Fu ? 0u : 0xFFu << (8 * c);
-                            } else {
-                                keep = ((y & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((y & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
-                            }
-                            strange |= keep != 0xFFFFFFFFu;
-                            v[j][q] = y & keep;
+                            const uint32_t y = v[j][q] & in;
+                            // the top bit of each element whose exponent is all ones (e4m3: that is 0x7F), then all its bits
+                            const uint32_t b = F8 ? ((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                            strange |= b;
+                            v[j][q] = y & ~((b - (b >> (F8 ? 7 : 15))) | b);
                         }
                     }
                 }
@@ -467,7 +465,7 @@ __global__ __launch_bounds__(PROMPT_THREADS, 2) void k_prompt_attn(const AttnArg
         // begins with the share is partial 2 b, one that begins inside it 2 b + 1
         const bool direct = st1 - st0 == cost;
         const int64_t pidx = 2 * (int64_t)blockIdx.x + (piece_at == share_lo ? 0 : 1);
-        const bool any_strange = __any(strange);
+        const bool any_strange = __any(strange != 0);
 #pragma unroll
         for (int mt = 0; mt < PMT; mt++) {
             const int x = x0 + mt * 16 + r16;
@@ -524,7 +522,10 @@ hipError_t launch_prompt(AttnArgs a, hipStream_t st) {
     a.shares = PROMPT_SHARES;
     hipLaunchKernelGGL(kern, dim3(a.shares), dim3(PROMPT_THREADS), lds, st, a);
     if (a.whole) return hipGetLastError();
-    hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 1>), dim3(a.T, (a.n_heads + 3) / 4), dim3(AT_THREADS), 0, st, a);
+    if ((int64_t)a.T * a.n_heads <= 32 * PROMPT_ROWS)
+        hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 4>), dim3(a.T, a.n_heads), dim3(4 * WAVE), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 1>), dim3(a.T, (a.n_heads + 3) / 4), dim3(AT_THREADS), 0, st, a);
     return hipGetLastError();
 }
 

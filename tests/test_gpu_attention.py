@@ -283,7 +283,7 @@ def test_paged_attention_every_shape(D, fp8, new):
 
 
 MANY_ROWS = [
-    # whole prompts and chunks: more than 64 rows (query token x head) per key-value head and request
+    # whole prompts and chunks: more than 128 rows (query token x head) per key-value head and request
     ([300, 200], [300, 150], 8, 2, 128, 16, False, 0, 0.0),
     ([700, 5, 410], [400, 1, 300], 4, 1, 256, 16, False, 0, 0.0),
     ([700, 5, 410], [400, 0, 300], 4, 1, 256, 32, True, 0, 30.0),
@@ -299,18 +299,32 @@ MANY_ROWS = [
 ]
 
 
+def many_rows_state(lens, new, Hq, Hkv, D, page, fp8, seed, pad):
+    """attn_state, with tables so wide (their far entries garbage) that the many-row kernel runs."""
+    W = max(max(-(-n // page) for n in lens) + 1, (1 << 25) // (sum(new) * Hq * page) + 1)
+    return attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=seed, pad=pad, W=W)
+
+
 @pytest.mark.parametrize("case", MANY_ROWS, ids=lambda c: "-".join(map(str, c[2:])).replace(" ", ""))
 def test_paged_attention_many_rows(case):
     lens, new, Hq, Hkv, D, page, fp8, window, cap = case
-    st = attn_state(lens, new, Hq, Hkv, D, page, fp8, seed=sum(lens), pad=3)
+    state = many_rows_state if window == 0 else attn_state
+    st = state(lens, new, Hq, Hkv, D, page, fp8, seed=sum(lens), pad=3)
     check_attn(st, run_attn(st, softcap=cap, window=window), softcap=cap, window=window)
+
+
+@pytest.mark.parametrize("D,fp8,window", [(64, False, 900), (128, True, 33), (256, False, 200)])
+def test_paged_attention_many_rows_windowed(D, fp8, window):
+    # enough rows that the many-row kernel runs: 1500 x 16 x (window + 1500 / 2) scores and more
+    st = attn_state([1700, 1800], [1500, 1600], 16, 2, D, 16, fp8, seed=window, pad=1)
+    check_attn(st, run_attn(st, softcap=20.0, window=window), softcap=20.0, window=window)
 
 
 @pytest.mark.parametrize("new", [80, 150])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_paged_attention_many_rows_every_shape(D, fp8, new):
-    st = attn_state([new + 550, new, new + 7], [new] * 3, 8, 2, D, 32, fp8, seed=new, pad=1)
+    st = many_rows_state([new + 550, new, new + 7], [new] * 3, 8, 2, D, 32, fp8, seed=new, pad=1)
     a = run_attn(st)
     check_attn(st, a)
     assert torch.equal(a.view(torch.int16), run_attn(st).view(torch.int16))
@@ -320,7 +334,7 @@ def test_paged_attention_many_rows_every_shape(D, fp8, new):
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [64, 256])
 def test_paged_attention_many_rows_that_see_nothing(D, fp8):
-    st = attn_state([0, 2, 400, 600], [90, 80, 200, 300], 4, 2, D, 16, fp8, seed=3)
+    st = many_rows_state([0, 2, 400, 600], [90, 80, 200, 300], 4, 2, D, 16, fp8, seed=3, pad=0)
     table = st["table"].clone()
     table[2] = -1                                    # request 2 has no page
     table[3, 9] = st["cache"].num_pages              # request 3 lacks positions 144..159 and 368..399
@@ -332,7 +346,7 @@ def test_paged_attention_many_rows_that_see_nothing(D, fp8):
 
 @pytest.mark.parametrize("D,fp8", [(64, False), (128, True), (256, False)])
 def test_paged_attention_many_rows_unseen_infinities_do_not_reach_a_row(D, fp8):
-    st = attn_state([700], [300], 4, 2, D, 16, fp8, seed=5)
+    st = many_rows_state([700], [300], 4, 2, D, 16, fp8, seed=5, pad=0)
     at = 650                                          # rows 0 .. 249 do not see it
     page, off = int(st["table"][0, at // 16]), at % 16
     if fp8:
