@@ -117,88 +117,102 @@ MOE_DEV int request_with(const AttnArgs& a, int t) {
 // waves (a unit in hundreds of shares; one token over 262,144 positions: 11 us
 // with 4 waves, 6 with 16), many rows one wave each (most of them in one share,
 // with nothing to do).
+//   Whole prompts: most rows have nothing to join, and looking that up is all that
+// their wave does: four rows a wave (8192 rows of 32 heads of 128: one row a wave
+// 86 us, four 56).
+constexpr int join_rows(bool GROW, int WPR) { return GROW && WPR == 1 ? 4 : 1; }
 template <int D, int RB, int STEP, bool GROW, int CH, int WPR>
 __global__ __launch_bounds__(WPR == 1 ? AT_THREADS : WPR * WAVE) void k_attn_join(const AttnArgs a) {
     constexpr int NW = AT_THREADS / WAVE, NC = D / CH, TC = CH / 4, GW = WAVE / TC, NG = GW * WPR;
     constexpr int U = 4;                   // shares in flight per thread
+    constexpr int TPW = join_rows(GROW, WPR);
     __shared__ float2 gml[WPR];
     __shared__ f32x4_t go[WPR][TC];
     const int l = lane_id(), w = uniform(threadIdx.x / WAVE);
-    const int t = blockIdx.x, y = WPR == 1 ? blockIdx.y * NW + w : blockIdx.y, hq = y / NC, c0 = y % NC * TC;
+    const int y = WPR == 1 ? blockIdx.y * NW + w : blockIdx.y, hq = y / NC, c0 = y % NC * TC;
     const int share = a.share[0];
-    const int s = request_with(a, t);
-    const Request rq = request_of<RB, STEP, GROW>(a, s);
-    if (hq >= a.n_heads || t < rq.row0 || t >= rq.row0 + rq.n) return;
-    const int nkv = a.kv.n_kv_heads, G = a.G;
-    const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
-    const int grp = row / RB, rr = row - grp * RB;
-    const int cost = rq.steps + rq.grow * grp;
-    const int u0 = a.base[s] + steps_before(rq, nkv, grp) + head * cost;    // the unit's first step
-    // (at most shares - 1 <= 511: the fp32 quotient is off by one at most)
-    auto share_of = [&](int u) {
-        const int q = (int)((float)u * __builtin_amdgcn_rcpf((float)share));
-        return q + ((int64_t)(q + 1) * share <= u ? 1 : 0) - ((int64_t)q * share > u ? 1 : 0);
-    };
-    const int b0 = share_of(u0), np = share_of(u0 + cost - 1) - b0 + 1;
-    if (np <= 1 || b0 < 0 || b0 + np > a.shares) return;     // (past the shares only with offsets that do not ascend)
-    const int first_odd = u0 == b0 * share ? 0 : 1;
-    const int e = l % TC, gr = (WPR == 1 ? 0 : w * GW) + l / TC;
-    float M = -__builtin_inff(), L = 0.f;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](float m2, float l2, f32x4_t v2) __attribute__((always_inline)) {
-        const float mn = fmaxf(M, m2), base = mn == -__builtin_inff() ? 0.f : mn;
-        const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(m2 - base);
-        L = L * f0 + l2 * f1;
-        o = o * f0 + v2 * f1;
-        M = mn;
-    };
-    for (int p0 = gr; p0 < np; p0 += NG * U) {
-        float2 x[U];
-        f32x4_t v[U];
-#pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int p = min(p0 + i * NG, np - 1);
-            const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
-            x[i] = a.ml[at];
-            v[i] = *reinterpret_cast<const f32x4_t*>(a.part + at * D + (c0 + e) * 4);
+    Request rq;
+    int s = 0;
+#pragma unroll 1
+    for (int n = 0; n < TPW; n++) {
+        const int t = blockIdx.x * TPW + n;
+        if (TPW > 1 && t >= a.T) return;
+        if (n == 0 || t >= rq.row0 + rq.n) {
+            s = request_with(a, t);
+            rq = request_of<RB, STEP, GROW>(a, s);
         }
+        if (hq >= a.n_heads || t < rq.row0 || t >= rq.row0 + rq.n) continue;
+        const int nkv = a.kv.n_kv_heads, G = a.G;
+        const int head = hq / G, row = (t - rq.row0) * G + (hq - head * G);
+        const int grp = row / RB, rr = row - grp * RB;
+        const int cost = rq.steps + rq.grow * grp;
+        const int u0 = a.base[s] + steps_before(rq, nkv, grp) + head * cost;    // the unit's first step
+        // (at most shares - 1 <= 511: the fp32 quotient is off by one at most)
+        auto share_of = [&](int u) {
+            const int q = (int)((float)u * __builtin_amdgcn_rcpf((float)share));
+            return q + ((int64_t)(q + 1) * share <= u ? 1 : 0) - ((int64_t)q * share > u ? 1 : 0);
+        };
+        const int b0 = share_of(u0), np = share_of(u0 + cost - 1) - b0 + 1;
+        if (np <= 1 || b0 < 0 || b0 + np > a.shares) continue;   // (past the shares only with offsets that do not ascend)
+        const int first_odd = u0 == b0 * share ? 0 : 1;
+        const int e = l % TC, gr = (WPR == 1 ? 0 : w * GW) + l / TC;
+        float M = -__builtin_inff(), L = 0.f;
+        f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+        auto add = [&](float m2, float l2, f32x4_t v2) __attribute__((always_inline)) {
+            const float mn = fmaxf(M, m2), base = mn == -__builtin_inff() ? 0.f : mn;
+            const float f0 = __builtin_amdgcn_exp2f(M - base), f1 = __builtin_amdgcn_exp2f(m2 - base);
+            L = L * f0 + l2 * f1;
+            o = o * f0 + v2 * f1;
+            M = mn;
+        };
+        for (int p0 = gr; p0 < np; p0 += NG * U) {
+            float2 x[U];
+            f32x4_t v[U];
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            if (p0 + i * NG >= np) break;
-            add(x[i].x, x[i].y, v[i]);
+            for (int i = 0; i < U; i++) {
+                const int p = min(p0 + i * NG, np - 1);
+                const int64_t at = (2 * (int64_t)(b0 + p) + (p == 0 ? first_odd : 0)) * RB + rr;
+                x[i] = a.ml[at];
+                v[i] = *reinterpret_cast<const f32x4_t*>(a.part + at * D + (c0 + e) * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                if (p0 + i * NG >= np) break;
+                add(x[i].x, x[i].y, v[i]);
+            }
         }
-    }
-    // the wave's groups: every lane ends with the sum over them, taken in the
-    // same order (its own pair's lower group first)
+        // the wave's groups: every lane ends with the sum over them, taken in the
+        // same order (its own pair's lower group first)
 #pragma unroll
-    for (int d = TC; d < WAVE; d <<= 1) {
-        const bool low = (l & d) == 0;
-        const float m2 = wave_xor(M, d), l2 = wave_xor(L, d);
-        f32x4_t v2;
+        for (int d = TC; d < WAVE; d <<= 1) {
+            const bool low = (l & d) == 0;
+            const float m2 = wave_xor(M, d), l2 = wave_xor(L, d);
+            f32x4_t v2;
 #pragma unroll
-        for (int i = 0; i < 4; i++) v2[i] = wave_xor(o[i], d);
-        const float m1 = M, l1 = L;
-        const f32x4_t v1 = o;
-        M = low ? m1 : m2; L = low ? l1 : l2; o = low ? v1 : v2;
-        add(low ? m2 : m1, low ? l2 : l1, low ? v2 : v1);
-    }
-    if constexpr (WPR > 1) {
-        if (l < TC) go[w][l] = o;
-        if (l == 0) gml[w] = make_float2(M, L);
-        __syncthreads();
-        if (threadIdx.x >= TC) return;
-        M = -__builtin_inff();
-        L = 0.f;
-        o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; i++) v2[i] = wave_xor(o[i], d);
+            const float m1 = M, l1 = L;
+            const f32x4_t v1 = o;
+            M = low ? m1 : m2; L = low ? l1 : l2; o = low ? v1 : v2;
+            add(low ? m2 : m1, low ? l2 : l1, low ? v2 : v1);
+        }
+        if constexpr (WPR > 1) {
+            if (l < TC) go[w][l] = o;
+            if (l == 0) gml[w] = make_float2(M, L);
+            __syncthreads();
+            if (threadIdx.x >= TC) continue;
+            M = -__builtin_inff();
+            L = 0.f;
+            o = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int i = 0; i < WPR; i++) add(gml[i].x, gml[i].y, go[i][e]);
-    } else if (l >= TC) {
-        return;
-    }
-    const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);
-    uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c0 + e);
+            for (int i = 0; i < WPR; i++) add(gml[i].x, gml[i].y, go[i][e]);
+        } else if (l >= TC) {
+            continue;
+        }
+        const float inv = L == 0.f ? 0.f : __builtin_amdgcn_rcpf(L);
+        uint16_t* dst = a.out + ((int64_t)t * a.n_heads + hq) * D + dim_of<D>(c0 + e);
 #pragma unroll
-    for (int i = 0; i < 4; i++) dst[(D == 64 ? 4 : 8) * i] = (uint16_t)pk_bf16(o[i] * inv, 0.f);
+        for (int i = 0; i < 4; i++) dst[(D == 64 ? 4 : 8) * i] = (uint16_t)pk_bf16(o[i] * inv, 0.f);
+    }
 }
 
 }  // namespace

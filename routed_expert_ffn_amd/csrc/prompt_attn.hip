@@ -525,7 +525,7 @@ hipError_t launch_prompt(AttnArgs a, hipStream_t st) {
     if ((int64_t)a.T * a.n_heads <= 32 * PROMPT_ROWS)
         hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 4>), dim3(a.T, a.n_heads), dim3(4 * WAVE), 0, st, a);
     else
-        hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 1>), dim3(a.T, (a.n_heads + 3) / 4), dim3(AT_THREADS), 0, st, a);
+        hipLaunchKernelGGL((k_attn_join<D, PROMPT_ROWS, TICK, true, D, 1>), dim3((a.T + join_rows(true, 1) - 1) / join_rows(true, 1), (a.n_heads + 3) / 4), dim3(AT_THREADS), 0, st, a);
     return hipGetLastError();
 }
 

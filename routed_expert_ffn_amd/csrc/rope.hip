@@ -13,6 +13,9 @@
 // them.  position * inv_freq and its remainder modulo 2 pi are taken in fp64
 // (at position 250,000 the fp32 product alone is off by 2^-24 * 250,000 =
 // 0.015 radians), the sine and cosine of the remainder in fp32.
+//   8,192 rows of 20 heads of 256 (168 MB): 34.4 us, 4.9 TB/s (a plain copy reaches 5.1);
+// 5 rows 3.6 us and 777 rows of 48 heads of 128 into an e4m3 cache (17.6 MB) 9.3 us are
+// latency: a load, the angles, two passes of lane moves and a store.
 #include "attn.h"
 #include "common.h"
 #include "stream.h"
@@ -231,7 +234,8 @@ hipError_t launch_d(const uint16_t* qkv, int64_t stride, int T, int n_heads, con
     const int groups = (n_heads + 2 * cache.n_kv_heads + HPW - 1) / HPW;
     // 8 rows per block (their keys' 16-byte chunks fill whole lines), the heads
     // split until there are about 1024 blocks; few rows: one row and one group
-    // of heads per wave
+    // of heads per wave.  Both sides: 777 x 12 groups 9.8 us with one row a wave and 10.6
+    // with 8 rows a block; 8192 x 10 groups 43 us and 37.
     if ((int64_t)T * groups <= 16384)
         launch_t<D, F8, 1, 1>(4, qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions,
                               slots, q_out, st);
