@@ -371,6 +371,7 @@ typedef struct {
  *   counts    [2] int32 out: the rows in use (q_offsets[S]) and the pages
  *             needed (sum take_s; more than n_free: the list was too short).
  * The outputs depend on the inputs alone, so a repeated call gives the same.
+ * They must not overlap the inputs (kv_len is not cached_len advanced in place).
  * Unsupported: S > 4096; page_size not a power of two in [16, 1024];
  * W * page_size > 2^30. */
 moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_t S, const int32_t* free_pages,

@@ -54,6 +54,8 @@ moe_status moe_kv_plan(const int32_t* cached_len, const int32_t* new_len, int32_
     if (!aligned4(cached_len) || !aligned4(new_len) || !aligned4(free_pages) || !aligned4(page_table) ||
         !aligned4(q_offsets) || !aligned4(kv_len) || !aligned4(positions) || !aligned4(slots) || !aligned4(counts))
         return MOE_ERR_UNSUPPORTED;
+    // every block reads the lengths while the first one writes these
+    if (kv_len == cached_len || kv_len == new_len || q_offsets == cached_len || q_offsets == new_len) return MOE_ERR_INVALID_ARG;
     return hip_status(launch_kv_plan(cached_len, new_len, S_, free_pages, n_free, shift, T, page_table, W, q_offsets,
                                      kv_len, positions, slots, counts, S(stream)));
 }

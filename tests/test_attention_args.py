@@ -49,6 +49,12 @@ def test_kv_plan_refuses(L):
     assert call(t=ctypes.c_void_p(0x10002)) == UNSUPPORTED
 
 
+def test_kv_plan_refuses_lengths_advanced_in_place(L):
+    p = [ctypes.c_void_p(0x10000 + 0x1000 * i) for i in range(9)]
+    for kv, offs in ((p[0], p[4]), (p[1], p[4]), (p[5], p[0]), (p[5], p[1])):
+        assert L.moe_kv_plan(p[0], p[1], 4, p[2], 3, 16, 8, p[3], 4, offs, kv, p[6], p[7], p[8], None) == INVALID
+
+
 def test_qk_norm_rope_refuses(L):
     base = dict(x=FAKE, xd=moe.BF16, st=20 * 128, T=3, h=16, c=cache(), qw=FAKE, kw=FAKE, f=FAKE, R=64, lay=0, p=FAKE,
                 s=FAKE, o=FAKE, eps=1e-6, rs=1.0)
