@@ -55,15 +55,15 @@ MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 // in result element i = p of each lane, row g, token l & 15.  Three quarters of
 // the MFMA's work is thrown away, which costs nothing (T <= 16 leaves the matrix
 // cores idle), and in return the loads need neither LDS nor narrow rows.
-// All of a block's loads go out at once.
+// A pass's loads go out at once: up to K = 2048 all of the block's.
 // More than 16 rows: TT tiles of 16, each with its own second operands and results.
 //   Bound: the weight's bytes, cold (a decode step reads each weight once).
-// 5 x 5120 x 2048: 21 MB in 6.1 us, 3.4 TB/s, of which about 2.5 us are the launch and
+// 5 x 5120 x 2048: 21 MB in 6.0 us, 3.5 TB/s, of which about 2.5 us are the launch and
 // the first load's way to memory and back; the library's product of the same size
 // is 8.9.
-//   KS (k steps per wave and pass): as many as give one pass, so that all loads are
-// out at once, up to 4 (more would spill): K = 2048, two passes of KS 1 7.0 us, one of
-// KS 2 6.1.
+//   KS, the k steps per wave and pass, and so the loads in flight: 5 x 5120 x 2048 6.7 us
+// with 1, 5.7 with 2, 7.6 with 4 (more registers, half of the steps past the end); 5 x 5120 x 8192 21.9,
+// 17.6, 18.2; 16 x 5120 x 8192 26.2, 22.0, 21.5; at K = 512 1 and 2 are the same.
 constexpr int ROWS_MAX_T = 32;
 constexpr int RW = 8;                      // waves per block
 
@@ -445,20 +445,15 @@ hipError_t launch_rows(const LinearArgs& a, int rows_per_block, hipStream_t st) 
     return hipGetLastError();
 }
 
-template <int KS, int OB>
-hipError_t launch_rows_k(const LinearArgs& a, hipStream_t st) {
-    // one block per CU while it has at most 32 weight rows (16 with more than 16 rows of x)
-    const int groups = (a.N + 3) / 4, rg = std::min(std::max((groups + 255) / 256, 1), a.T <= 16 ? 8 : 4);
-    if (a.T <= 16) {
-        if (rg == 1) return launch_rows<1, KS, 1, OB>(a, 4, st);
-        if (rg == 2) return launch_rows<2, KS, 1, OB>(a, 8, st);
-        if (rg <= 4) return launch_rows<4, KS, 1, OB>(a, 4 * rg, st);
-        return launch_rows<8, KS, 1, OB>(a, 4 * rg, st);
-    }
-    if constexpr (KS == 1) {
-        return rg <= 2 ? launch_rows<2, 1, 2, OB>(a, 4 * rg, st) : launch_rows<4, 1, 2, OB>(a, 4 * rg, st);
-    }
-    return hipErrorInvalidValue;
+template <int OB>
+hipError_t launch_few(const LinearArgs& a, hipStream_t st) {
+    // one block per CU while it has at most 32 weight rows
+    const int groups = (a.N + 3) / 4, rg = std::min(std::max((groups + 255) / 256, 1), 8);
+    if (a.T > 16) return launch_rows<2, 1, 2, OB>(a, 4 * rg, st);            // (N <= 2048: rg is 1 or 2)
+    if (rg == 1) return launch_rows<1, 2, 1, OB>(a, 4, st);
+    if (rg == 2) return launch_rows<2, 2, 1, OB>(a, 8, st);
+    if (rg <= 4) return launch_rows<4, 2, 1, OB>(a, 4 * rg, st);
+    return launch_rows<8, 2, 1, OB>(a, 4 * rg, st);
 }
 
 template <int BT, int BN, int BK, int ST, int WN, int KG, int BPC, int OB>
@@ -480,9 +475,7 @@ hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
     // narrow weights hide (24 x 2048 x 8192: 19.5 us, tiles 23) and wide ones do not (24 x 5120 x 8192:
     // 38, tiles 24); from 33 rows on tiles are as good throughout.
     if (a.T <= 16 || (a.T <= ROWS_MAX_T && a.N <= 2048)) {
-        if (a.K <= 1024 || a.T > 16) return launch_rows_k<1, OB>(a, st);
-        if (a.K <= 2048) return launch_rows_k<2, OB>(a, st);
-        return launch_rows_k<4, OB>(a, st);
+        return launch_few<OB>(a, st);
     }
     auto tiles = [&](int b) { return (int64_t)((a.T + b - 1) / b) * ((a.N + b - 1) / b); };
     auto rounds = [&](int b) { return (tiles(b) + 255) / 256; };             // tiles a CU is given

@@ -234,9 +234,10 @@ hipError_t launch_d(const uint16_t* qkv, int64_t stride, int T, int n_heads, con
     const int groups = (n_heads + 2 * cache.n_kv_heads + HPW - 1) / HPW;
     // 8 rows per block (their keys' 16-byte chunks fill whole lines), the heads
     // split until there are about 1024 blocks; few rows: one row and one group
-    // of heads per wave.  Both sides: 777 x 12 groups 9.8 us with one row a wave and 10.6
-    // with 8 rows a block; 8192 x 10 groups 43 us and 37.
-    if ((int64_t)T * groups <= 16384)
+    // of heads per wave.  Both sides, one row a wave first: 256 rows x 10 groups 4.7 us against 6.1,
+    // 777 x 10 8.5 against 8.3, 777 x 12 (e4m3) 10.1 against 10.5, 1600 x 10 14.1 against 11.3, 8192 x 10 52
+    // against 39.
+    if ((int64_t)T * groups <= 10240)
         launch_t<D, F8, 1, 1>(4, qkv, stride, T, n_heads, cache, qw, kw, eps, inv_freq, R, inter, rope_scale, positions,
                               slots, q_out, st);
     else
