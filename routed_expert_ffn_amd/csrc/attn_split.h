@@ -37,7 +37,8 @@ namespace {
 
 constexpr int AT_THREADS = 256;             // of the few-row kernel and of the one-wave joins
 // What a piece costs besides its own positions (its q rows, first loads and
-// join), in positions: short requests would otherwise pile up in few shares.
+// join), in positions: short requests would otherwise pile up in few shares (40 requests of
+// up to 600 positions 14 us; at 512 positions a piece 16).
 constexpr int PIECE_COST = 128;
 constexpr float LOG2E = 1.44269504088896341f;
 
@@ -77,14 +78,17 @@ MOE_DEV Request request_of(const AttnArgs& a, int s) {
     r.first = L - r.n;
     r.len = (int)min((int64_t)L, (int64_t)a.W << a.kv.page_shift);
     const int lo = a.window > 0 ? max(r.first - a.window + 1, 0) : 0;
-    r.grow = GROW && a.window == 0 ? (RB + STEP * a.G / 2) / (STEP * a.G) : 0;
+    // (rows before position 0 or behind the table see nothing more: their cost would outgrow int32)
+    r.grow = GROW && a.window == 0 && r.first >= 0 && r.len == L ? (RB + STEP * a.G / 2) / (STEP * a.G) : 0;
     const int hi = GROW ? (int)min((int64_t)r.len, (int64_t)max(r.first, 0) + RB / a.G) : r.len;
     r.units = (int)(((uint32_t)(r.n * a.G) + RB - 1) / RB) * a.kv.n_kv_heads;      // (T * n_heads fits int32)
     r.steps = (max(hi - lo, 0) + STEP - 1) / STEP + PIECE_COST / STEP;
     return r;
 }
 // steps of the units before row group grp
-MOE_DEV int steps_before(const Request& r, int nkv, int grp) { return nkv * (r.steps * grp + r.grow * (int)((uint32_t)(grp * (grp - 1)) / 2)); }
+MOE_DEV int steps_before(const Request& r, int nkv, int grp) {
+    return nkv * (r.steps * grp + r.grow * (int)((uint32_t)grp * (uint32_t)(grp - 1) / 2));
+}
 
 // the page table through the scalar cache (nothing writes it while the kernel runs)
 typedef const __attribute__((address_space(4))) int32_t* table_ptr;

@@ -30,8 +30,7 @@
 //
 // Bound by HBM at few rows: each cached byte is used for 16 MT rows at a time.  One row over
 // 262,144 positions (16 heads of 256 on 2, 537 MB): 86 us, 6.2 TB/s, and 6 us for the join; 64 requests
-// of one row and up to 8192 positions, e4m3 (166 MB), 37 and 5 us, 4.4 TB/s: the shares' ends
-// and the conversions of e4m3.  5 rows over 4096 positions, 13 and 5 us for 8.5 MB, are
+// of one row and up to 8192 positions, e4m3 (166 MB), 37 and 5 us, 4.5 TB/s.  5 rows over 4096 positions, 13 and 5 us for 8.5 MB, are
 // latency: a block's 16 positions per wave pass q, the first tile, one softmax, the
 // join through LDS and a partial result of 40 rows.
 #include "attn_split.h"

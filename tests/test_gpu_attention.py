@@ -344,6 +344,12 @@ def test_paged_attention_many_rows_that_see_nothing(D, fp8):
     assert bool((got[:168] == 0).all()) and bool((got[170:370] == 0).all())
 
 
+@pytest.mark.parametrize("lens", [[2000], [640], [300]])             # past the table, up to it, more rows than positions
+def test_paged_attention_many_rows_lengths_past_the_table(lens):
+    st = attn_state(lens, [1000], 64, 1, 64, 16, False, seed=4, W=40)
+    check_attn(st, run_attn(st))
+
+
 @pytest.mark.parametrize("D,fp8", [(64, False), (128, True), (256, False)])
 def test_paged_attention_many_rows_unseen_infinities_do_not_reach_a_row(D, fp8):
     st = many_rows_state([700], [300], 4, 2, D, 16, fp8, seed=5, pad=0)
