@@ -159,8 +159,7 @@ __global__ __launch_bounds__(RW * WAVE, 2) void k_linear_rows(const uint16_t* __
 // {0, 2, 3, 1}[(row >> 2) & 3].  No conflicts counted.
 //   KG 2: two groups of waves take half of each K step each and add their sums at
 // the end through LDS: with one block per CU twice the waves hide what a K step
-// waits for.  48 x 1000 x 8192: 33 us with one group, 21 with two; at K = 512 the
-// adding costs more than it gives (4.7 us against 5.1).
+// waits for (48 x 1000 x 8192, 4 stages each: 33 us with one group, 21 with two).
 //   Bound: with many tiles the matrix cores and their feeding.  8192 x 2048 x 4096
 // 115 us, 1.19 PFLOP/s (1.36 PFLOP/s is what a large library product reaches; its
 // own time here is 92); 8 waves of 128 x 64 outputs each, two per SIMD, so that one
@@ -491,7 +490,13 @@ hipError_t launch_ob(const LinearArgs& a, hipStream_t st) {
                   c256 = rounds(256) * 44;
     if (c256 < c128 && c256 < c64) return launch_tile<256, 256, 32, 4, 4, 1, 1, OB>(a, st);
     if (c128 < c64) return launch_tile<128, 128, 32, 4, 2, 1, 2, OB>(a, st);
-    if (tiles(64) <= 256 && a.K >= 2048) return launch_tile<64, 64, 128, 4, 2, 2, 1, OB>(a, st);
+    // One 64-square tile per CU: six stages, or from K = 2048 on two k groups.  Weights
+    // from memory, 4 stages against 6: 333 x 1000 x 1088 7.8 us and 6.9, 333 x 1000 x 1920 13.9 and 11.2
+    // (8 stages: 7.2 and 11.4).  Six stages against two groups: weights in the caches, 48 x 1000 x 8192
+    // 26.2 us and 21.2, 400 x 2048 x 8192 31.7 and 26.9, 333 x 1000 x 2048 9.5 and 8.8; from memory the two
+    // are within 5 percent (32.9 and 34.1, 35.8 and 35.3, 11.3 and 11.7).
+    if (tiles(64) <= 256)
+        return a.K >= 2048 ? launch_tile<64, 64, 128, 4, 2, 2, 1, OB>(a, st) : launch_tile<64, 64, 64, 6, 2, 1, 1, OB>(a, st);
     return launch_tile<64, 64, 64, 4, 2, 1, 2, OB>(a, st);
 }
 
